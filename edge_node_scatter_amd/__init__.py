@@ -435,3 +435,7 @@ def gie_zonal_scatter_normalized(coupling: torch.Tensor, radial: torch.Tensor, e
     not carry); ``zs_forward_normalized`` returns it as a plain tensor."""
     return _GieZonalScatterNormalized.apply(coupling, radial, env, csr.rowptr, csr.perm,
                                             csr.dst32, csr.n_nodes, csr.order)
+
+
+from .block import (AdamW, block_join, block_norm, grouped_mm, sorted_groups,  # noqa: E402, F401
+                    zs_block_join, zs_block_join_backward, zs_grouped_mm, zs_grouped_mm_backward)

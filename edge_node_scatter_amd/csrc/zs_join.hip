@@ -1,0 +1,501 @@
+// The gated residual join between two norms and its gradients, gfx950.
+//
+//   u = zn w_post, zn = z rz, rz = (mean z^2 + eps)^(-1/2)
+//   y = x + scale s u, s = sigmoid(gate);  h = y ry w_pre, ry likewise
+//
+// backward, with t = gh w_pre and everything recomputed from the inputs:
+//   gx = gy + ry t - y ry^3 mean(t y)
+//   b = gx s, q = b scale, r = q w_post
+//   gz = rz (r - zn mean(r zn)),  ggate = q u (1 - s)
+//   gscale = sum b u, gpost = sum q zn, gpre = sum gh y ry   (over the rows)
+//
+// One pass over memory: a row stays in the registers of L lanes, which hold its
+// 16-byte chunks l, l + L, ...; the row sums cross the lanes (and, above a
+// wavefront, LDS).  The parameter gradients are summed over a workgroup's rows
+// in registers, then over its row slots in LDS, and the workgroups' partial
+// sums are added in order by a second kernel.
+#include "zs_block_internal.h"
+#include "zs_tile.h"
+
+namespace zs {
+
+namespace {
+
+template <typename T>
+struct Chunk {
+    static constexpr int V = 16 / sizeof(T);
+    __device__ static void unpack(u32x4 raw, float (&f)[V]) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t bits = raw[i];
+                f[i] = __builtin_bit_cast(float, bits);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __builtin_bit_cast(float, raw[i] << 16);
+                f[2 * i + 1] = __builtin_bit_cast(float, raw[i] & 0xffff0000u);
+            }
+        }
+    }
+    __device__ static u32x4 pack(const float (&f)[V]) {
+        union {
+            T e[V];
+            u32x4 v;
+        } u;
+#pragma unroll
+        for (int i = 0; i < V; ++i) u.e[i] = T(f[i]);
+        return u.v;
+    }
+};
+
+// Chunk `chunk` of a row of c elements (zeros outside).
+template <typename T>
+__device__ inline u32x4 load_chunk(const T* row, int chunk, int c, bool vec) {
+    constexpr int V = Chunk<T>::V;
+    const int left = c - chunk * V;
+    if (vec) return left > 0 ? *reinterpret_cast<const u32x4*>(row + chunk * V) : u32x4{0, 0, 0, 0};
+    return load_partial(row + chunk * V, left);
+}
+template <typename T>
+__device__ inline void store_chunk(T* row, int chunk, int c, bool vec, u32x4 v) {
+    constexpr int V = Chunk<T>::V;
+    const int left = c - chunk * V;
+    if (vec) {
+        if (left > 0) *reinterpret_cast<u32x4*>(row + chunk * V) = v;
+        return;
+    }
+    union {
+        u32x4 v;
+        T e[V];
+    } u;
+    u.v = v;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (i < left) row[chunk * V + i] = u.e[i];
+}
+// V fp32 parameters of a chunk.
+template <int V>
+__device__ inline void load_param(const float* p, int chunk, int c, bool vec, float (&f)[V]) {
+    const int left = c - chunk * V;
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const f32x4 t = left > 0 ? *reinterpret_cast<const f32x4*>(p + chunk * V + i)
+                                     : f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) f[i + q] = t[q];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = i < left ? p[chunk * V + i] : 0.0f;
+    }
+}
+
+// Sums of N values over the L lanes of a row.  Above a wavefront the row is the
+// workgroup's and the wavefronts meet in LDS: `region` alternates, so that one
+// barrier per sum is enough (a region is written again only behind the next
+// sum's barrier).
+template <int L, int N>
+__device__ inline void row_sum(float (&v)[N], float* lds, int& region) {
+#pragma unroll
+    for (int h = (L < 64 ? L : 64) / 2; h >= 1; h >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], h, 64);
+    if constexpr (L > 64) {
+        constexpr int W = L / 64;
+        float* at = lds + region * W * 2;
+        region ^= 1;
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) at[wave * 2 + i] = v[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) s += at[w * 2 + i];
+            v[i] = s;
+        }
+    }
+}
+
+// sigmoid(a) and 1 - sigmoid(a), both without cancellation.
+__device__ inline void sigmoid2(float a, float& s, float& o) {
+    const float t = __expf(-__builtin_fabsf(a));
+    const float d = __builtin_amdgcn_rcpf(1.0f + t);
+    const float small = t * d;
+    s = a >= 0.0f ? d : small;
+    o = a >= 0.0f ? small : d;
+    if (a != a) s = o = a;
+}
+
+template <typename T>
+struct JoinParams {
+    const T *x, *z, *gate;
+    const float *scale, *w_post, *w_pre;
+    int64_t ldx, ldz, ldg, n_rows;
+    int c, gate_kind;   // 0: none, 1: one per row, 2: one per channel
+    float eps, inv_c;
+    bool vec;
+    T *y, *h;
+    const T *gy, *gh;
+    T *gx, *gz, *ggate;
+    float *gscale, *gpost, *gpre, *partial;
+};
+
+constexpr int threads_of(int L) { return L > 256 ? L : 256; }
+
+template <typename T, int L, int NV>
+__global__ __launch_bounds__(threads_of(L)) void zs_join_kernel(const JoinParams<T> p) {
+    constexpr int V = Chunk<T>::V;
+    constexpr int kRowsOf = threads_of(L) / L;
+    __shared__ float lds[2 * (L > 64 ? L / 64 : 1) * 2];
+    int region = 0;
+    const int l = threadIdx.x % L, slot = threadIdx.x / L;
+    for (int64_t base = int64_t(blockIdx.x) * kRowsOf; base < p.n_rows;
+         base += int64_t(gridDim.x) * kRowsOf) {
+        const int64_t row = base + slot;
+        const bool live = row < p.n_rows;
+        const int c = live ? p.c : 0;
+        float y[NV][V];
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            Chunk<T>::unpack(load_chunk(p.x + row * p.ldx, l + j * L, c, p.vec), y[j]);
+        if (p.z) {
+            u32x4 zr[NV], ar[NV];
+            float row_gate = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) zr[j] = load_chunk(p.z + row * p.ldz, l + j * L, c, p.vec);
+            if (p.gate_kind == 2) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    ar[j] = load_chunk(p.gate + row * p.ldg, l + j * L, c, p.vec);
+            } else if (p.gate_kind == 1 && live) {
+                row_gate = float(p.gate[row * p.ldg]);
+            }
+            float s[1] = {0.0f};
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                float z[V];
+                Chunk<T>::unpack(zr[j], z);
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[0] = __builtin_fmaf(z[i], z[i], s[0]);
+            }
+            row_sum<L>(s, lds, region);
+            const float rz = 1.0f / sqrtf(__builtin_fmaf(s[0], p.inv_c, p.eps));
+            float gate_s = 1.0f, gate_o = 0.0f;
+            if (p.gate_kind == 1) sigmoid2(row_gate, gate_s, gate_o);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                float z[V], a[V], sc[V], wp[V];
+                Chunk<T>::unpack(zr[j], z);
+                load_param<V>(p.scale, l + j * L, c, p.vec, sc);
+                load_param<V>(p.w_post, l + j * L, c, p.vec, wp);
+                if (p.gate_kind == 2) Chunk<T>::unpack(ar[j], a);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float g = gate_s, o;
+                    if (p.gate_kind == 2) sigmoid2(a[i], g, o);
+                    y[j][i] = __builtin_fmaf(sc[i] * g, z[i] * rz * wp[i], y[j][i]);
+                }
+                if (live) store_chunk(p.y + row * p.c, l + j * L, c, p.vec, Chunk<T>::pack(y[j]));
+            }
+        }
+        if (p.w_pre) {
+            float s[1] = {0.0f};
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[0] = __builtin_fmaf(y[j][i], y[j][i], s[0]);
+            row_sum<L>(s, lds, region);
+            const float ry = 1.0f / sqrtf(__builtin_fmaf(s[0], p.inv_c, p.eps));
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                float w[V];
+                load_param<V>(p.w_pre, l + j * L, c, p.vec, w);
+#pragma unroll
+                for (int i = 0; i < V; ++i) w[i] = y[j][i] * ry * w[i];
+                if (live) store_chunk(p.h + row * p.c, l + j * L, c, p.vec, Chunk<T>::pack(w));
+            }
+        }
+    }
+}
+
+template <typename T, int L, int NV>
+__global__ __launch_bounds__(threads_of(L)) void zs_join_bwd_kernel(const JoinParams<T> p) {
+    constexpr int V = Chunk<T>::V;
+    constexpr int kThreads = threads_of(L), kRowsOf = kThreads / L;
+    __shared__ float lds[2 * (L > 64 ? L / 64 : 1) * 2];
+    __shared__ float sums[kRowsOf > 1 ? kThreads * V : 1];
+    int region = 0;
+    const int l = threadIdx.x % L, slot = threadIdx.x / L;
+    float acc[3][NV][V];   // scale, w_post, w_pre
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[q][j][i] = 0.0f;
+    for (int64_t base = int64_t(blockIdx.x) * kRowsOf; base < p.n_rows;
+         base += int64_t(gridDim.x) * kRowsOf) {
+        const int64_t row = base + slot;
+        const bool live = row < p.n_rows;
+        const int c = live ? p.c : 0;
+        u32x4 zr[NV], ar[NV], yr[NV], hr[NV];
+        float y[NV][V];
+        float row_gate = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int at = l + j * L;
+            zr[j] = p.z ? load_chunk(p.z + row * p.ldz, at, c, p.vec) : u32x4{0, 0, 0, 0};
+            Chunk<T>::unpack(load_chunk(p.x + row * p.ldx, at, c, p.vec), y[j]);
+            ar[j] = p.gate_kind == 2 ? load_chunk(p.gate + row * p.ldg, at, c, p.vec)
+                                     : u32x4{0, 0, 0, 0};
+            yr[j] = p.gy ? load_chunk(p.gy + row * p.c, at, c, p.vec) : u32x4{0, 0, 0, 0};
+            hr[j] = p.gh ? load_chunk(p.gh + row * p.c, at, c, p.vec) : u32x4{0, 0, 0, 0};
+        }
+        if (p.gate_kind == 1 && live) row_gate = float(p.gate[row * p.ldg]);
+        float rz = 0.0f, gate_s = 1.0f, gate_o = 0.0f;
+        if (p.z) {
+            float s[1] = {0.0f};
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                float z[V];
+                Chunk<T>::unpack(zr[j], z);
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[0] = __builtin_fmaf(z[i], z[i], s[0]);
+            }
+            row_sum<L>(s, lds, region);
+            rz = 1.0f / sqrtf(__builtin_fmaf(s[0], p.inv_c, p.eps));
+            if (p.gate_kind == 1) sigmoid2(row_gate, gate_s, gate_o);
+        }
+        float s2[2] = {0.0f, 0.0f};   // y^2, t y
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int at = l + j * L;
+            if (p.z) {
+                float z[V], a[V], sc[V], wp[V];
+                Chunk<T>::unpack(zr[j], z);
+                load_param<V>(p.scale, at, c, p.vec, sc);
+                load_param<V>(p.w_post, at, c, p.vec, wp);
+                if (p.gate_kind == 2) Chunk<T>::unpack(ar[j], a);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float g = gate_s, o;
+                    if (p.gate_kind == 2) sigmoid2(a[i], g, o);
+                    y[j][i] = __builtin_fmaf(sc[i] * g, z[i] * rz * wp[i], y[j][i]);
+                }
+            }
+            if (p.w_pre) {
+                float gh[V], w[V];
+                Chunk<T>::unpack(hr[j], gh);
+                load_param<V>(p.w_pre, at, c, p.vec, w);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    s2[0] = __builtin_fmaf(y[j][i], y[j][i], s2[0]);
+                    s2[1] = __builtin_fmaf(gh[i] * w[i], y[j][i], s2[1]);
+                }
+            }
+        }
+        float ry = 0.0f, my = 0.0f;   // my = ry^3 mean(t y)
+        if (p.w_pre) {
+            row_sum<L>(s2, lds, region);
+            ry = 1.0f / sqrtf(__builtin_fmaf(s2[0], p.inv_c, p.eps));
+            my = ry * ry * ry * (s2[1] * p.inv_c);
+        }
+        float s3[2] = {0.0f, 0.0f};   // r zn, q u (1 - s)
+        float gx[NV][V];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int at = l + j * L;
+            Chunk<T>::unpack(yr[j], gx[j]);
+            if (p.w_pre) {
+                float gh[V], w[V];
+                Chunk<T>::unpack(hr[j], gh);
+                load_param<V>(p.w_pre, at, c, p.vec, w);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    acc[2][j][i] = __builtin_fmaf(gh[i] * ry, y[j][i], acc[2][j][i]);
+                    gx[j][i] = __builtin_fmaf(ry, gh[i] * w[i], gx[j][i]) - my * y[j][i];
+                }
+            }
+            if (live) store_chunk(p.gx + row * p.c, at, c, p.vec, Chunk<T>::pack(gx[j]));
+            if (p.z) {
+                float z[V], a[V], sc[V], wp[V], ga[V];
+                Chunk<T>::unpack(zr[j], z);
+                load_param<V>(p.scale, at, c, p.vec, sc);
+                load_param<V>(p.w_post, at, c, p.vec, wp);
+                if (p.gate_kind == 2) Chunk<T>::unpack(ar[j], a);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float g = gate_s, o = gate_o;
+                    if (p.gate_kind == 2) sigmoid2(a[i], g, o);
+                    const float zn = z[i] * rz, u = zn * wp[i];
+                    const float b = gx[j][i] * g, q = b * sc[i], r = q * wp[i];
+                    acc[0][j][i] = __builtin_fmaf(b, u, acc[0][j][i]);
+                    acc[1][j][i] = __builtin_fmaf(q, zn, acc[1][j][i]);
+                    s3[0] = __builtin_fmaf(r, zn, s3[0]);
+                    ga[i] = q * u * o;
+                    s3[1] += ga[i];
+                    gx[j][i] = r;
+                }
+                if (p.gate_kind == 2 && live)
+                    store_chunk(p.ggate + row * p.c, at, c, p.vec, Chunk<T>::pack(ga));
+            }
+        }
+        if (p.z) {
+            row_sum<L>(s3, lds, region);
+            if (p.gate_kind == 1 && live && l == 0) p.ggate[row] = T(s3[1]);
+            const float mz = s3[0] * p.inv_c;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                float z[V];
+                Chunk<T>::unpack(zr[j], z);
+#pragma unroll
+                for (int i = 0; i < V; ++i) z[i] = rz * (gx[j][i] - z[i] * rz * mz);
+                if (live) store_chunk(p.gz + row * p.c, l + j * L, c, p.vec, Chunk<T>::pack(z));
+            }
+        }
+    }
+    // sums over the workgroup's row slots, then out: [3][c] per workgroup
+    float* out = p.partial + int64_t(blockIdx.x) * 3 * p.c;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if constexpr (kRowsOf > 1) {
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < V; ++i) sums[(slot * L + l) * V + i] = acc[q][j][i];
+                __syncthreads();
+                for (int e = threadIdx.x; e < L * V; e += kThreads) {
+                    const int ch = j * L * V + e;
+                    float s = 0.0f;
+                    for (int k = 0; k < kRowsOf; ++k) s += sums[k * L * V + e];
+                    if (ch < p.c) out[int64_t(q) * p.c + ch] = s;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int ch = (j * L + l) * V + i;
+                    if (ch < p.c) out[int64_t(q) * p.c + ch] = acc[q][j][i];
+                }
+            }
+        }
+    }
+}
+
+// Adds the workgroups' partial sums in order: 32 columns a workgroup, 32 lanes
+// of partial rows each, joined in LDS.
+__global__ __launch_bounds__(1024) void zs_join_sum_kernel(const float* partial, int count, int c,
+                                                           float* gscale, float* gpost,
+                                                           float* gpre) {
+    __shared__ float lds[32][33];
+    const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+    float s = 0.0f;
+    if (col < 3 * c) {
+#pragma unroll 4
+        for (int i = part; i < count; i += 32) s += partial[int64_t(i) * 3 * c + col];
+    }
+    lds[part][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (part == 0 && col < 3 * c) {
+        s = 0.0f;
+        for (int i = 0; i < 32; ++i) s += lds[i][threadIdx.x];
+        float* out = col < c ? gscale : (col < 2 * c ? gpost : gpre);
+        if (out) out[col % c] = s;
+    }
+}
+
+template <typename T>
+JoinParams<T> params(const JoinArgs& a) {
+    constexpr int V = Chunk<T>::V;
+    JoinParams<T> p{};
+    p.x = static_cast<const T*>(a.x), p.z = static_cast<const T*>(a.z);
+    p.gate = static_cast<const T*>(a.gate);
+    p.scale = a.scale, p.w_post = a.w_post, p.w_pre = a.w_pre;
+    p.ldx = a.ldx, p.ldz = a.ldz, p.ldg = a.ldg, p.n_rows = a.n_rows;
+    p.c = a.c;
+    // a gate per channel of one channel is the gate per row
+    p.gate_kind = a.gate_width == 0 ? 0 : (a.gate_width == 1 ? 1 : 2);
+    p.eps = a.eps, p.inv_c = 1.0f / float(a.c);
+    p.y = static_cast<T*>(a.y), p.h = static_cast<T*>(a.h);
+    p.gy = static_cast<const T*>(a.gy), p.gh = static_cast<const T*>(a.gh);
+    p.gx = static_cast<T*>(a.gx), p.gz = static_cast<T*>(a.gz), p.ggate = static_cast<T*>(a.ggate);
+    p.gscale = a.gscale, p.gpost = a.gpost, p.gpre = a.gpre, p.partial = a.partial;
+    const auto on16 = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
+    p.vec = a.c % V == 0 && a.ldx % V == 0 && on16(a.x) && on16(a.y) && on16(a.h) && on16(a.gy) &&
+            on16(a.gh) && on16(a.gx) && on16(a.gz) && on16(a.scale) && on16(a.w_post) &&
+            on16(a.w_pre);
+    if (a.z) p.vec = p.vec && a.ldz % V == 0 && on16(a.z);
+    if (p.gate_kind == 2)
+        p.vec = p.vec && a.ldg % V == 0 && on16(a.gate) && on16(a.ggate);
+    return p;
+}
+
+constexpr int64_t kMaxPartials = 1024;
+
+template <typename T, int L, int NV>
+hipError_t run(const JoinArgs& a, bool backward, hipStream_t stream) {
+    const JoinParams<T> p = params<T>(a);
+    constexpr int rows = threads_of(L) / L;
+    const int64_t want = (a.n_rows + rows - 1) / rows;
+    if (!backward) {
+        const unsigned grid = unsigned(want < 8192 ? want : 8192);
+        zs_join_kernel<T, L, NV><<<grid, threads_of(L), 0, stream>>>(p);
+        return hipGetLastError();
+    }
+    const int64_t cap = join_workspace(a.n_rows, a.c) / (12 * int64_t(a.c));
+    const unsigned grid = unsigned(want < cap ? want : cap);
+    if (grid > 0) {
+        zs_join_bwd_kernel<T, L, NV><<<grid, threads_of(L), 0, stream>>>(p);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    zs_join_sum_kernel<<<(3 * a.c + 31) / 32, 1024, 0, stream>>>(a.partial, int(grid), a.c,
+                                                                 a.gscale, a.gpost, a.gpre);
+    return hipGetLastError();
+}
+
+// Lanes and chunks per lane by the row's width in chunks: the fewest lanes that
+// hold a row in one chunk each up to a wavefront, then up to four chunks a lane
+// of a wavefront, then a workgroup.
+template <typename T>
+hipError_t dispatch(const JoinArgs& a, bool backward, hipStream_t stream) {
+    const int chunks = (a.c + Chunk<T>::V - 1) / Chunk<T>::V;
+    if (chunks <= 1) return run<T, 1, 1>(a, backward, stream);
+    if (chunks <= 2) return run<T, 2, 1>(a, backward, stream);
+    if (chunks <= 4) return run<T, 4, 1>(a, backward, stream);
+    if (chunks <= 8) return run<T, 8, 1>(a, backward, stream);
+    if (chunks <= 16) return run<T, 16, 1>(a, backward, stream);
+    if (chunks <= 32) return run<T, 32, 1>(a, backward, stream);
+    if (chunks <= 64) return run<T, 64, 1>(a, backward, stream);
+    if (chunks <= 128) return run<T, 64, 2>(a, backward, stream);
+    if (chunks <= 192) return run<T, 64, 3>(a, backward, stream);
+    if (chunks <= 256) return run<T, 256, 1>(a, backward, stream);
+    if (chunks <= 512) return run<T, 256, 2>(a, backward, stream);
+    if (chunks <= 1024) return run<T, 256, 4>(a, backward, stream);
+    if constexpr (sizeof(T) == 4) return run<T, 1024, 2>(a, backward, stream);
+    return hipErrorInvalidValue;   // wider than ZS_MAX_JOIN_WIDTH: refused before
+}
+
+}  // namespace
+
+size_t join_workspace(int64_t n_rows, int64_t c) {
+    int64_t parts = n_rows < kMaxPartials ? n_rows : kMaxPartials;
+    return size_t(parts * 3 * c * 4);
+}
+
+hipError_t launch_join(const JoinArgs& a, bool bf16, hipStream_t stream) {
+    return bf16 ? dispatch<__bf16>(a, false, stream) : dispatch<float>(a, false, stream);
+}
+
+hipError_t launch_join_backward(const JoinArgs& a, bool bf16, hipStream_t stream) {
+    return bf16 ? dispatch<__bf16>(a, true, stream) : dispatch<float>(a, true, stream);
+}
+
+}  // namespace zs
