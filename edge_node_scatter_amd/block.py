@@ -87,7 +87,8 @@ def _typed(t: torch.Tensor, name: str, dtype: torch.dtype | None = None,
 def _rows(t: torch.Tensor) -> torch.Tensor:
     """A matrix whose rows are contiguous: a view with a row stride is taken in
     place, anything else is copied."""
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.stride(0) < 0:
+    row, col = t.stride()
+    if (col != 1 and t.shape[1] > 1) or row < 0:
         t = t.contiguous()
     return t
 
@@ -216,8 +217,9 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, groups: Csr) -> torch.Tensor:
 
 # ---- residual join ---------------------------------------------------------------------------------
 
-def _join_inputs(x, z, gate, scale, w_post, w_pre):
-    x = _typed(x, "x")
+def _join_refusal(x, z, gate, scale, w_post, w_pre):
+    """Raises for what is wrong with a join's inputs, one by one."""
+    _typed(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be (M, c)")
     dev, c = x.device, x.shape[1]
@@ -230,23 +232,42 @@ def _join_inputs(x, z, gate, scale, w_post, w_pre):
         _typed(z, "z", x.dtype, dev)
         if z.shape != x.shape:
             raise ValueError("z must have x's shape")
-        z = _rows(z)
         if scale is None or w_post is None:
             raise ValueError("z needs scale and w_post")
         if gate is not None:
             _typed(gate, "gate", x.dtype, dev)
             if tuple(gate.shape) not in ((x.shape[0], c), (x.shape[0], 1)):
                 raise ValueError("gate must be (M, c) or (M, 1)")
-            gate = _rows(gate)
-    vectors = []
     for name, t in (("scale", scale), ("w_post", w_post), ("w_pre", w_pre)):
         if t is not None:
             _typed(t, name, torch.float32, dev)
             if tuple(t.shape) != (c,):
                 raise ValueError(f"{name} must be ({c},)")
-            t = t.contiguous()
-        vectors.append(t)
-    return _rows(x), z, gate, *vectors
+
+
+def _join_inputs(x, z, gate, scale, w_post, w_pre):
+    """The inputs, checked, as the kernels can read them."""
+    F32, dev, shape, dtype = torch.float32, x.device, x.shape, x.dtype
+    ok = x.is_cuda and dtype in DTYPES and len(shape) == 2
+    if ok:
+        c = shape[1:]
+        if z is None:
+            ok = gate is None and scale is None and w_post is None and w_pre is not None
+        else:
+            ok = (scale is not None and w_post is not None and z.shape == shape
+                  and z.dtype == dtype and z.device == dev
+                  and scale.shape == c and scale.dtype == F32 and scale.device == dev
+                  and w_post.shape == c and w_post.dtype == F32 and w_post.device == dev
+                  and (gate is None or gate.dtype == dtype and gate.device == dev
+                       and (gate.shape == shape or gate.shape == (shape[0], 1))))
+        ok = ok and (w_pre is None or w_pre.shape == c and w_pre.dtype == F32
+                     and w_pre.device == dev)
+    if not ok:
+        _join_refusal(x, z, gate, scale, w_post, w_pre)
+        raise ValueError("inputs do not fit a join")
+    return (_rows(x), z if z is None else _rows(z), gate if gate is None else _rows(gate),
+            *(t if t is None or t.is_contiguous() else t.contiguous()
+              for t in (scale, w_post, w_pre)))
 
 
 def _join_args(x, z, gate, scale, w_post, w_pre, eps):
@@ -391,8 +412,11 @@ class AdamW:
             self._dense(state[n], f"state[{n!r}]", self._dtype(n), self._shape(n))
         self.state = dict(state)
         self._table = (_Tensor * len(self.params))()
-        for t, off, p in zip(self._table, self.offsets, self.params):
-            t.n, t.state_offset = p.numel(), off
+        # the table as 64-bit words: param, grad, copy, n, state_offset, grad_dtype and reserved
+        self._words = (ctypes.c_int64 * (6 * len(self.params))).from_buffer(self._table)
+        self._shapes = [p.shape for p in self.params]
+        self._words[3::6] = self._sizes = [p.numel() for p in self.params]
+        self._words[4::6] = self.offsets
 
     def _shape(self, name):
         return (self.total // STATE_BLOCK,) if name.endswith("_scale") else (self.total,)
@@ -414,19 +438,7 @@ class AdamW:
             grads = [p.grad for p in self.params]
         if len(grads) != len(self.params):
             raise ValueError("grads must be one tensor for each parameter")
-        for i, (t, p, g) in enumerate(zip(self._table, self.params, grads)):
-            if g is None:
-                t.n = 0
-                continue
-            if g.dtype not in DTYPES:
-                raise TypeError(f"grads[{i}] must be float32 or bfloat16, got {g.dtype}")
-            if g.device != self.device or g.shape != p.shape:
-                raise ValueError(f"grads[{i}] must be {tuple(p.shape)} on {self.device}")
-            if not g.is_contiguous() or not p.is_contiguous():
-                raise ValueError(f"grads[{i}] and its parameter must be contiguous")
-            t.n = p.numel()
-            t.param, t.grad, t.grad_dtype = p.data_ptr(), g.data_ptr(), DTYPES[g.dtype]
-            t.copy = None if self.copies is None else self.copies[i].data_ptr()
+        self._fill(grads)
         s = self.state
         c = _Config(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
                     s["step"] + 1)
@@ -440,6 +452,32 @@ class AdamW:
                            _ptr(s["v_scale"]), self.total, s["seed"] & 0xFFFFFFFF)
         _check("zs_adamw_step", status)
         s["step"] += 1
+
+    def _fill(self, grads) -> None:
+        """The table's addresses and types for this step.  All tensors are looked
+        at in a few passes over the lists; what a pass finds is named one by one."""
+        T, words, params, sizes = torch.Tensor, self._words, self.params, self._sizes
+        if any(g is None for g in grads):
+            # a tensor without a gradient gets a size of 0 and its own memory's address
+            sizes = [0 if g is None else n for g, n in zip(grads, sizes)]
+            grads = [p if g is None else g for g, p in zip(grads, params)]
+        index = {self.device.index}
+        types = [DTYPES.get(g.dtype) for g in grads]
+        if (None in types or [g.shape for g in grads] != self._shapes
+                or [p.shape for p in params] != self._shapes
+                or set(map(T.get_device, grads)) != index or set(map(T.get_device, params)) != index
+                or not all(map(T.is_contiguous, grads)) or not all(map(T.is_contiguous, params))):
+            for i, (g, shape) in enumerate(zip(grads, self._shapes)):
+                self._dense(params[i], f"params[{i}]", torch.float32, shape)
+                if g.dtype not in DTYPES:
+                    raise TypeError(f"grads[{i}] must be float32 or bfloat16, got {g.dtype}")
+                self._dense(g, f"grads[{i}]", g.dtype, shape)
+        words[0::6] = list(map(T.data_ptr, params))
+        words[1::6] = list(map(T.data_ptr, grads))
+        if self.copies is not None:
+            words[2::6] = list(map(T.data_ptr, self.copies))
+        words[3::6] = sizes
+        words[5::6] = types
 
     def moments(self) -> tuple[torch.Tensor, torch.Tensor]:
         """(m, v) flat in fp32: the state itself with 32 bits, the values that

@@ -1,8 +1,8 @@
 // Grouped products y[i] = x[i] op(w[g(i)]) for gfx950.
 //
 // One workgroup forms a BM x BN tile of one group's rows: x rows (gathered
-// through perm) and the group's weights go through LDS in stages of 128 bytes
-// of k, two buffers deep, and the matrix cores accumulate in fp32.
+// through perm) and the group's weights go through LDS in stages of KB
+// bytes of k, S buffers deep, and the matrix cores accumulate in fp32.
 #include "zs_block_internal.h"
 #include "zs_tile.h"
 
@@ -23,35 +23,24 @@ struct MmParams {
 
 constexpr int pow2_at_least(int v) { return v <= 32 ? 32 : v <= 64 ? 64 : v <= 128 ? 128 : 256; }
 
-template <typename T>
-__device__ inline void store4(T* p, f32x4 v) {
-    if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<f32x4*>(p) = v;
-    } else {
-        *reinterpret_cast<bf16x4*>(p) = __builtin_convertvector(v, bf16x4);
-    }
-}
-
 // WT: weights stored [n][k] (row form in LDS), else [k][n] (sum form).
-// AV, BV: the operand's chunks of 16 bytes start on 16 bytes and lie wholly
-// inside or outside it, so they are loaded straight to LDS.
-template <typename T, int BM, int BN, int WM, int WN, bool WT, bool AV, bool BV>
+// VEC: the operands' chunks of 16 bytes start on 16 bytes and lie wholly
+// inside or outside them, so they are loaded straight to LDS; otherwise
+// elements are loaded one by one.
+template <typename T, int BM, int BN, int WM, int WN, int KB, int S, bool WT, bool VEC>
 __global__ __launch_bounds__(WM * WN * 64) void zs_gmm_kernel(const MmParams<T> p) {
     constexpr int kWaves = WM * WN;
     constexpr int E = 16 / sizeof(T);              // elements of a chunk
-    constexpr int BK = kStageBytes / sizeof(T);
+    constexpr int BK = KB / sizeof(T);
     constexpr int LN = pow2_at_least(BN);          // width of the weight tile in LDS
-    constexpr int kABytes = BM * kStageBytes, kBBytes = LN * kStageBytes;
-    constexpr int IA = BM / 8 / kWaves, IB = LN / 8 / kWaves;   // loads per wavefront and stage
+    constexpr int kABytes = BM * KB, kBytes = kABytes + LN * KB;
+    constexpr int kRows = 1024 / KB, kChunks = KB / 16;   // of a wavefront's load, of a row
+    constexpr int IA = BM / kRows / kWaves, IB = LN / kRows / kWaves;   // loads per wavefront and stage
     constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
     static_assert(IA >= 1 && IB >= 1 && MT >= 1 && NT >= 1, "tile too small for its wavefronts");
     extern __shared__ __align__(16) char lds[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t item = xcd_item(blockIdx.x, gridDim.x);
-    const int64_t slot = item / p.n_tiles;
-    const int n0 = int(item - slot * p.n_tiles) * BN;
-
     // groups 0 and n_groups + 1 are the rows before the first and behind the
     // last offset: they get zeros
     const auto start = [&](int64_t v) -> int64_t {
@@ -60,8 +49,9 @@ __global__ __launch_bounds__(WM * WN * 64) void zs_gmm_kernel(const MmParams<T> 
         const int64_t o = p.offsets[v - 1];
         return o < 0 ? 0 : (o > p.n_rows ? p.n_rows : o);
     };
-    const TileOf tile = find_tile(slot, p.n_groups + 2, BM, start);
-    if (tile.group < 0 || tile.begin >= tile.end) return;
+    const TileOf tile = find_work(blockIdx.x, gridDim.x, p.n_tiles, p.n_groups + 2, BM, 0, start);
+    if (tile.group < 0) return;
+    const int n0 = __builtin_amdgcn_readfirstlane(tile.sub) * BN;
     const int group = __builtin_amdgcn_readfirstlane(tile.group) - 1;
     const bool in_group = group >= 0 && group < p.n_groups;
 
@@ -87,9 +77,9 @@ __global__ __launch_bounds__(WM * WN * 64) void zs_gmm_kernel(const MmParams<T> 
         int a_k[IA];
 #pragma unroll
         for (int i = 0; i < IA; ++i) {
-            const int m = (wave * IA + i) * 8 + (lane >> 3);
+            const int m = (wave * IA + i) * kRows + lane / kChunks;
             const int64_t r = row_at(m);
-            a_k[i] = ((lane & 7) ^ row_swizzle(m)) * E;
+            a_k[i] = ((lane % kChunks) ^ row_swizzle<KB>(m)) * E;
             a_ptr[i] = r < 0 ? nullptr : p.x + r * p.ldx + a_k[i];
         }
         const T* b_ptr[IB];
@@ -98,8 +88,8 @@ __global__ __launch_bounds__(WM * WN * 64) void zs_gmm_kernel(const MmParams<T> 
 #pragma unroll
         for (int i = 0; i < IB; ++i) {
             if constexpr (WT) {
-                const int c = (wave * IB + i) * 8 + (lane >> 3);
-                b_k[i] = ((lane & 7) ^ row_swizzle(c)) * E;
+                const int c = (wave * IB + i) * kRows + lane / kChunks;
+                b_k[i] = ((lane % kChunks) ^ row_swizzle<KB>(c)) * E;
                 b_n[i] = n0 + c;
                 b_ptr[i] = c < BN && b_n[i] < p.n ? w + int64_t(b_n[i]) * p.ldw + b_k[i] : nullptr;
             } else {
@@ -117,7 +107,7 @@ __global__ __launch_bounds__(WM * WN * 64) void zs_gmm_kernel(const MmParams<T> 
                 const int left = p.k - k0 - a_k[i];
                 const bool in = a_ptr[i] && left > 0;
                 const T* src = a_ptr[i] + k0;
-                if constexpr (AV)
+                if constexpr (VEC)
                     load_to_lds(in ? static_cast<const void*>(src) : zero_chunk, lds_offset(to));
                 else
                     *reinterpret_cast<u32x4*>(to + lane * 16) = load_partial(src, in ? left : 0);
@@ -128,40 +118,23 @@ __global__ __launch_bounds__(WM * WN * 64) void zs_gmm_kernel(const MmParams<T> 
                 const bool in = b_ptr[i] && k0 + b_k[i] < p.k;
                 const T* src = b_ptr[i] + (WT ? int64_t(k0) : int64_t(k0) * p.ldw);
                 const int left = WT ? p.k - k0 - b_k[i] : p.n - b_n[i];
-                if constexpr (BV)
+                if constexpr (VEC)
                     load_to_lds(in ? static_cast<const void*>(src) : zero_chunk, lds_offset(to));
                 else
                     *reinterpret_cast<u32x4*>(to + lane * 16) = load_partial(src, in ? left : 0);
             }
         };
-        load(0, lds);
-        wait_loads();
-        __syncthreads();
-        int cur = 0;
-        for (int k0 = 0; k0 < p.k; k0 += BK) {
-            const char* at = lds + cur * (kABytes + kBBytes);
-            cur ^= 1;
-            if (k0 + BK < p.k) load(k0 + BK, lds + cur * (kABytes + kBBytes));
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                typename Frag<T>::V a[MT], b[NT];
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    if constexpr (WT)
-                        b[j] = read_row_frag<T>(at + kABytes, wn * NT + j, s, lane);
-                    else
-                        b[j] = read_sum_frag<T, LN>(at + kABytes, wn * NT + j, s, lane);
-                }
-#pragma unroll
-                for (int i = 0; i < MT; ++i) a[i] = read_row_frag<T>(at, wm * MT + i, s, lane);
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) acc[i][j] = mma16(b[j], a[i], acc[i][j]);
-            }
-            wait_loads();
-            __syncthreads();
-        }
+        product_loop<T, MT, NT, KB, S, kBytes, IA + IB>(
+            (p.k + BK - 1) / BK, lds, acc, [&](int i, char* buf) { load(i * BK, buf); },
+            [&](const char* at, int i, int s) {
+                return read_row_frag<T, KB>(at, wm * MT + i, s, lane);
+            },
+            [&](const char* at, int j, int s) {
+                if constexpr (WT)
+                    return read_row_frag<T, KB>(at + kABytes, wn * NT + j, s, lane);
+                else
+                    return read_sum_frag<T, LN>(at + kABytes, wn * NT + j, s, lane);
+            });
     }
 
     const bool wide = p.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(p.y) % (4 * sizeof(T)) == 0;
@@ -184,16 +157,24 @@ __global__ __launch_bounds__(WM * WN * 64) void zs_gmm_kernel(const MmParams<T> 
     }
 }
 
-template <typename T, int BM, int BN, int WM, int WN, bool WT, bool AV, bool BV>
+template <typename T, int BM, int BN, int WM, int WN, int KB, int S, bool WT, bool VEC>
 hipError_t run(const GmmArgs& a, hipStream_t stream) {
+    constexpr int BK = KB / sizeof(T);
     MmParams<T> p{static_cast<const T*>(a.x), static_cast<const T*>(a.w), static_cast<T*>(a.y),
                   a.offsets, a.perm, a.ldx, a.ldw, a.w_group, a.ldy, a.n_rows, a.n_groups,
                   a.k, a.n, (a.n + BN - 1) / BN};
     const int64_t slots = a.n_rows / BM + a.n_groups + 2;
     const int64_t grid = slots * p.n_tiles;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    constexpr int bytes = 2 * (BM + pow2_at_least(BN)) * kStageBytes;
-    auto* kernel = zs_gmm_kernel<T, BM, BN, WM, WN, WT, AV, BV>;
+    // no more buffers than stages: short sums leave LDS for more workgroups
+    const int stages = (a.k + BK - 1) / BK;
+    const int bytes = (stages < S ? stages : S) * (BM + pow2_at_least(BN)) * KB;
+    auto* kernel = zs_gmm_kernel<T, BM, BN, WM, WN, KB, S, WT, VEC>;
+    if (bytes > 65536) {
+        const hipError_t err = hipFuncSetAttribute(
+            reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (err != hipSuccess) return err;
+    }
     kernel<<<dim3(unsigned(grid)), WM * WN * 64, bytes, stream>>>(p);
     return hipGetLastError();
 }
@@ -202,12 +183,22 @@ template <typename T, bool WT>
 hipError_t dispatch(const GmmArgs& a, hipStream_t stream) {
     constexpr int E = 16 / sizeof(T);
     const auto on16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-    const bool av = on16(a.x) && a.ldx % E == 0 && a.k % E == 0;
-    const bool bv = on16(a.w) && a.ldw % E == 0 && a.w_group % E == 0 && (WT ? a.k : a.n) % E == 0;
-    if (av && bv) return run<T, 128, 128, 2, 2, WT, true, true>(a, stream);
-    if (av) return run<T, 128, 128, 2, 2, WT, true, false>(a, stream);
-    if (bv) return run<T, 128, 128, 2, 2, WT, false, true>(a, stream);
-    return run<T, 128, 128, 2, 2, WT, false, false>(a, stream);
+    const bool vec = on16(a.x) && a.ldx % E == 0 && a.k % E == 0 && on16(a.w) && a.ldw % E == 0 &&
+                     a.w_group % E == 0 && (WT || a.n % E == 0);
+    if (!vec) return run<T, 64, 64, 2, 2, 128, 2, WT, false>(a, stream);
+    const auto tiles = [&](int bm, int bn) {
+        return (a.n_rows / bm + a.n_groups) * ((a.n + bn - 1) / bn);
+    };
+    if (tiles(128, 128) < 256) return run<T, 32, 64, 2, 2, 128, 4, WT, true>(a, stream);
+    const int bn = tile_side(a.n, true);
+    if (bn == 128) {
+        if constexpr (sizeof(T) == 2)
+            if (tiles(256, 256) >= 256) return run<T, 256, 256, 2, 4, 128, 2, WT, true>(a, stream);
+        return run<T, 128, 128, 2, 2, 128, 2, WT, true>(a, stream);
+    }
+    if (bn == 96) return run<T, 128, 96, 4, 1, 128, 2, WT, true>(a, stream);
+    if (bn == 64) return run<T, 128, 64, 4, 1, 128, 2, WT, true>(a, stream);
+    return run<T, 128, 32, 4, 1, 128, 2, WT, true>(a, stream);
 }
 
 }  // namespace

@@ -1,13 +1,13 @@
 // LDS tiles and matrix-core fragments shared by the grouped products and their
 // weight gradient (gfx950).
 //
-// A product stage covers 128 bytes of the summed index: 32 fp32 or 64 bf16
-// steps.  Tiles lie in LDS in 16-byte chunks, in one of two forms:
+// A product stage covers KB = 64 or 128 bytes of the summed index (16 or 32
+// fp32, 32 or 64 bf16 steps).  Tiles lie in LDS in 16-byte chunks, in one of two forms:
 //   row form ("R"): one tile row per kept index (a row of x, a column of y),
-//     the summed index contiguous, 128 bytes a row;
+//     the summed index contiguous, KB bytes a row;
 //   sum form ("S"): one tile row per summed index, the kept index contiguous
 //     (weights stored [k][n], and both operands of the weight gradient).
-// Both forms are 128 * (kept indices) bytes.  Chunks are permuted within their
+// Both forms are KB * (kept indices) bytes.  Chunks are permuted within their
 // row (XOR with a function of the row) so that a fragment's reads fall on
 // different banks.
 //
@@ -32,8 +32,6 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef short i16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kStageBytes = 128;
-
 // 16 bytes of zeros that lanes outside an operand load instead.
 static __device__ __align__(16) const uint32_t zero_chunk[4] = {0, 0, 0, 0};
 
@@ -54,7 +52,17 @@ __device__ inline void load_to_lds(const void* g, uint32_t lds) {
                  : "s"(lds), "v"(g)
                  : "memory");
 }
-__device__ inline void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All but the latest N of this wavefront's loads have arrived.
+template <int N>
+__device__ inline void wait_loads() {
+    static_assert(N >= 0 && N < 64, "vmcnt has 6 bits");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Workgroup barrier that waits for LDS accesses but leaves loads to LDS in
+// flight; wait_loads() says which of those have arrived.
+__device__ inline void tile_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
 
 template <typename T>
 struct Frag;
@@ -78,20 +86,24 @@ __device__ inline f32x4 mma16(f32x4 a, f32x4 b, f32x4 acc) {
 }
 
 // ---- row form -------------------------------------------------------------
-__device__ inline int row_swizzle(int row) { return (row >> 1) & 7; }
+// 16 rows at one chunk fall on all 64 banks.
+template <int KB>
+__device__ inline int row_swizzle(int row) {
+    return KB == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
+}
 
 // Fragment of tile rows 16 t .. 16 t + 15, sub-stage s.
-template <typename T>
+template <typename T, int KB>
 __device__ inline typename Frag<T>::V read_row_frag(const char* tile, int t, int s, int lane) {
     const int row = t * 16 + (lane & 15);
-    const int chunk = (s * 4 + (lane >> 4)) ^ row_swizzle(row);
-    return *reinterpret_cast<const typename Frag<T>::V*>(tile + row * kStageBytes + chunk * 16);
+    const int chunk = (s * 4 + (lane >> 4)) ^ row_swizzle<KB>(row);
+    return *reinterpret_cast<const typename Frag<T>::V*>(tile + row * KB + chunk * 16);
 }
 
 // ---- sum form, W kept indices per row ---------------------------------------
 template <typename T, int W>
 __device__ inline int sum_swizzle(int k) {
-    if (sizeof(T) == 4) return 4 * ((k >> 2) & (W / 16 >= 4 ? 3 : W / 16 - 1));
+    if constexpr (sizeof(T) == 4) return 4 * ((k >> 2) & (W / 16 >= 4 ? 3 : W / 16 - 1));
     constexpr int pairs = W / 16;   // 32-byte pairs of chunks in a row
     return 2 * (((k & 3) | ((k >> 1) & 4)) & (pairs - 1));
 }
@@ -151,54 +163,209 @@ __device__ inline u32x4 load_partial(const T* p, int count) {
     return u.v;
 }
 
+template <typename T>
+__device__ inline void store4(T* p, f32x4 v) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<f32x4*>(p) = v;
+    } else {
+        *reinterpret_cast<bf16x4*>(p) = __builtin_convertvector(v, bf16x4);
+    }
+}
+
+// The product loop over `stages` stages, S buffers of kBytes deep.  issue(i, buf)
+// starts the loads of stage i (kLoads per wavefront); read_a(buf, i, s) and
+// read_b(buf, j, s) read fragments of sub-stage s.
+//
+// Fragments are read ahead of the matrix instructions that use them: the b of
+// the next sub-stage and A row fragments up to `ahead` rows on, so that the
+// LDS works while the matrix cores do; read together behind the barrier the two
+// took turns (256 x 256 tiles in bf16 kept the matrix cores busy 53 % of the
+// time).  The barrier of a new stage therefore comes `ahead` rows before the end
+// of the old one, when the last of its fragments have been read; its buffer is
+// then free for stage i + S.  Behind the last stage the reads ahead fetch
+// values that nothing uses, from the workgroup's own buffers.
+template <typename T, int MT, int NT, int KB, int S, int kBytes, int kLoads, typename Issue,
+          typename ReadA, typename ReadB>
+__device__ inline void product_loop(int stages, char* lds, f32x4 (&acc)[MT][NT], Issue issue,
+                                    ReadA read_a, ReadB read_b) {
+    using V = typename Frag<T>::V;
+    constexpr int NS = KB / 64, ahead = MT < 4 ? MT : 4;
+    if (stages <= 0) return;
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+        if (i < stages) issue(i, lds + i * kBytes);
+    if (stages >= S)
+        wait_loads<(S - 1) * kLoads>();
+    else
+        wait_loads<0>();
+    tile_barrier();
+    V a[MT], b[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) b[j] = read_b(lds, j, 0);
+#pragma unroll
+    for (int i = 0; i < ahead; ++i) a[i] = read_a(lds, i, 0);
+    int cur = 0;
+    for (int stage = 0; stage < stages; ++stage) {
+        char* at = lds + cur * kBytes;
+        const int next = cur + 1 == S ? 0 : cur + 1;
+        // one buffer only: there is one stage
+        char* behind = stages > next ? lds + next * kBytes : lds;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            const char* from = at;
+            V b_next[NT], a_next[ahead];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                if (i == MT - ahead) {
+                    if (s == NS - 1) {
+                        // stage + 1 has arrived when at most the S - 2 behind it are in flight
+                        if (stage + S <= stages)
+                            wait_loads<(S - 2) * kLoads>();
+                        else
+                            wait_loads<0>();
+                        tile_barrier();
+                        if (stage + S < stages) issue(stage + S, at);
+                        from = behind;
+                    }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) b_next[j] = read_b(from, j, (s + 1) % NS);
+                }
+                if (i + ahead < MT)
+                    a[i + ahead] = read_a(at, i + ahead, s);
+                else
+                    a_next[i + ahead - MT] = read_a(from, i + ahead - MT, (s + 1) % NS);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) acc[i][j] = mma16(b[j], a[i], acc[i][j]);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) b[j] = b_next[j];
+#pragma unroll
+            for (int i = 0; i < ahead; ++i) a[i] = a_next[i];
+        }
+        cur = next;
+    }
+}
+
+// Side of the tiles that cover `width`: as few tiles as sides of 128 need, as
+// narrow as covers it, so that little of a tile is padding while wide operands
+// are still read as few times as 128 allows.
+inline int tile_side(int64_t width, bool with96) {
+    const int64_t tiles = (width + 127) / 128;
+    for (int s : {32, 64, 96})
+        if ((s != 96 || with96) && s * tiles >= width) return s;
+    return 128;
+}
+
 // ---- ragged groups ------------------------------------------------------------
-// Tiles of ragged groups without a prefix sum over them: group v, which starts
-// at sorted position e(v), owns the tile slots from e(v) / step + v up to the
-// next group's.  That many slots always hold its ceil(rows / step) tiles, slots
-// increase with v, and all groups together have n_rows / step + groups of
-// them, so a grid of that size can be launched without reading the offsets
-// on the host; a slot without rows ends at once.
+// The tiles of ragged groups are numbered without the host reading the offsets:
+// the grid holds as many workgroups as there can be tiles (one part-filled tile
+// a group), each finds its own, and those behind the last end at once.
 struct TileOf {
     int64_t begin, end;   // sorted positions of the tile
-    int64_t group_end;
     int group;            // -1: no tile
     int index;            // tile number within the group
     int tiles;            // tiles of the group (0: empty group)
+    int sub;              // which of the tile's `subs` work items
 };
 
-// start(v), v = 0 .. count: the groups' clamped boundaries.  64 boundaries are
-// probed at a time, one per lane.
+__device__ inline TileOf tile_at(int64_t v, int64_t index, int64_t step, int64_t a, int64_t b) {
+    TileOf t;
+    t.tiles = b > a ? int((uint32_t(b - a) + uint32_t(step) - 1) / uint32_t(step)) : 0;
+    t.begin = a + index * step;
+    t.end = t.begin + step < b ? t.begin + step : b;
+    if (t.end < t.begin) t.end = t.begin;
+    t.group = int(v);
+    t.index = int(index);
+    t.sub = 0;
+    return t;
+}
+
+// Up to this many groups a wavefront adds up all groups' tiles, 64 at a time.
+constexpr int kCountedGroups = 512;
+
+// The work of workgroup `id`: start(v), v = 0 .. count, are the groups' clamped
+// boundaries; a group has a tile for each `step` of its rows, `least` at least,
+// and a tile `subs` work items.  Workgroups go to the 8 XCDs in turn, so XCD x,
+// which holds the ids x, x + 8, ..., gets an eighth of the items, in one piece:
+// neighbouring items share its L2, and no XCD has more tiles than another
+// (dealing out the ids of the second scheme, whose empty ones fall anywhere,
+// left some XCDs a tile more than they have room for at a time: 16384 rows of
+// 8 equal groups, 512 -> 512 in fp32, took 113 us instead of 83).
+//
+// With more groups, group v owns the slots from start(v) / step + v up to the
+// next group's: never fewer than its tiles, increasing with v, and a search over
+// the boundaries, 64 probes at a time, finds a slot's group.
 template <typename Start>
-__device__ inline TileOf find_tile(int64_t slot, int64_t count, int64_t step, Start start) {
+__device__ inline TileOf find_work(uint32_t id, uint32_t grid, int subs, int64_t count,
+                                   int64_t step, int least, Start start) {
     const int lane = threadIdx.x & 63;
+    TileOf none{};
+    none.group = -1;
+    const uint32_t xcd = id % 8, nth = id / 8;
+    if (count <= kCountedGroups) {
+        uint32_t before[kCountedGroups / 64], total = 0;   // inclusive, per lane; of all
+        const int chunks = int((count + 63) / 64);
+#pragma unroll
+        for (int c = 0; c < kCountedGroups / 64; ++c) {
+            before[c] = 0;
+            if (c >= chunks) continue;
+            const int64_t v = c * 64 + lane;
+            uint32_t n = 0;
+            if (v < count) {
+                const int64_t a = start(v), b = start(v + 1);
+                n = b > a ? (uint32_t(b - a) + uint32_t(step) - 1) / uint32_t(step) : 0;
+                n = n < uint32_t(least) ? uint32_t(least) : n;
+            }
+#pragma unroll
+            for (int h = 1; h < 64; h <<= 1) {
+                const uint32_t o = __shfl_up(n, h, 64);
+                if (lane >= h) n += o;
+            }
+            before[c] = total + n;
+            total = __builtin_amdgcn_readlane(before[c], 63);
+        }
+        const uint64_t items = uint64_t(total) * uint32_t(subs);
+        const uint64_t per = items / 8, rest = items % 8;
+        if (nth >= per + (xcd < rest ? 1 : 0)) return none;
+        const uint64_t item = xcd * per + (xcd < rest ? xcd : rest) + nth;
+        const uint32_t tile = uint32_t(item / uint32_t(subs));
+        uint32_t base = 0;
+#pragma unroll
+        for (int c = 0; c < kCountedGroups / 64; ++c) {
+            if (c >= chunks) continue;
+            const uint32_t last = __builtin_amdgcn_readlane(before[c], 63);
+            if (tile < last) {
+                const int l = __popcll(__ballot(before[c] <= tile));   // lanes before the group
+                const uint32_t first = l > 0 ? uint32_t(__shfl(before[c], l - 1, 64)) : base;
+                const int64_t v = c * 64 + l;
+                TileOf t = tile_at(v, tile - first, step, start(v), start(v + 1));
+                t.sub = int(item - uint64_t(tile) * uint32_t(subs));
+                return t;
+            }
+            base = last;
+        }
+        return none;
+    }
+    const uint32_t per = grid / 8, rest = grid % 8;
+    const uint32_t item = xcd * per + (xcd < rest ? xcd : rest) + nth;
+    const int64_t slot = item / uint32_t(subs);
     int64_t lo = 0, hi = count;
     while (hi - lo > 1) {
         const int64_t stride = (hi - lo + 63) / 64;
         const int64_t v = lo + lane * stride;
-        const bool below = v < hi && start(v) / step + v <= slot;
+        const bool below = v < hi && uint32_t(start(v)) / uint32_t(step) + v <= slot;
         const int n = __popcll(__ballot(below));
         const int64_t next = lo + (n > 0 ? n - 1 : 0) * stride;
         hi = next + stride < hi ? next + stride : hi;
         lo = next;
     }
-    TileOf t;
-    const int64_t a = start(lo), b = start(lo + 1);
-    const int64_t rel = slot - (a / step + lo);
-    t.tiles = b > a ? int((b - a + step - 1) / step) : 0;
-    t.begin = a + rel * step;
-    t.end = t.begin + step < b ? t.begin + step : b;
-    t.group_end = b;
-    t.index = int(rel);
-    t.group = rel >= 0 && (t.begin < b || rel == 0) ? int(lo) : -1;
-    if (t.end < t.begin) t.end = t.begin;
+    const int64_t a = start(lo);
+    const int64_t index = slot - (uint32_t(a) / uint32_t(step) + lo);
+    if (index < 0) return none;
+    TileOf t = tile_at(lo, index, step, a, start(lo + 1));
+    if (index >= (t.tiles > least ? t.tiles : least)) return none;
+    t.sub = int(item - uint32_t(slot) * uint32_t(subs));
     return t;
-}
-
-// Hands each XCD (workgroups go to the 8 XCDs in turn) a contiguous range of
-// work items, so that neighbouring items share an L2.
-__device__ inline int64_t xcd_item(int64_t id, int64_t total) {
-    const int64_t per = total / 8, rest = total % 8, xcd = id % 8, i = id / 8;
-    return xcd * per + (xcd < rest ? xcd : rest) + i;
 }
 
 }  // namespace zs

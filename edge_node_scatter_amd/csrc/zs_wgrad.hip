@@ -30,27 +30,30 @@ __device__ inline int64_t clamp_offset(const int32_t* offsets, int64_t v, int64_
     return o < 0 ? 0 : (o > n_rows ? n_rows : o);
 }
 
-template <typename T, int BA, int BN, int WA, int WN, bool AV, bool BV>
+constexpr int pow2_at_least(int v) { return v <= 32 ? 32 : v <= 64 ? 64 : 128; }
+constexpr int kIndexRows = 1024;   // row indices kept in LDS at a time
+
+// VEC as in the grouped products.
+template <typename T, int BA, int BN, int WA, int WN, int KB, int S, bool VEC>
 __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T> p) {
     constexpr int kWaves = WA * WN;
     constexpr int E = 16 / sizeof(T);
-    constexpr int BR = kStageBytes / sizeof(T);    // rows of a stage
-    constexpr int kABytes = BA * kStageBytes, kBBytes = BN * kStageBytes;
-    constexpr int IA = BA / 8 / kWaves, IB = BN / 8 / kWaves;
+    constexpr int BR = KB / sizeof(T);    // rows of a stage
+    constexpr int LN = pow2_at_least(BN);
+    constexpr int kABytes = BA * KB, kBytes = kABytes + LN * KB;
+    constexpr int IA = BA * KB / 1024 / kWaves, IB = LN * KB / 1024 / kWaves;
     constexpr int AT = BA / WA / 16, NT = BN / WN / 16;
     static_assert(IA >= 1 && IB >= 1 && AT >= 1 && NT >= 1, "tile too small for its wavefronts");
     extern __shared__ __align__(16) char lds[];
+    __shared__ int32_t index[kIndexRows];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t item = xcd_item(blockIdx.x, gridDim.x);
-    const int tiles = p.k_tiles * p.n_tiles;
-    const int64_t slot = item / tiles;
-    const int in_slot = int(item - slot * tiles);
-    const int a0 = in_slot / p.n_tiles * BA, n0 = in_slot % p.n_tiles * BN;
     const auto start = [&](int64_t v) { return clamp_offset(p.offsets, v, p.n_rows); };
-    const TileOf tile = find_tile(slot, p.n_groups, p.piece, start);
+    const TileOf tile = find_work(blockIdx.x, gridDim.x, p.k_tiles * p.n_tiles, p.n_groups,
+                                  p.piece, 1, start);
     if (tile.group < 0) return;
-    if (tile.index > 0 && tile.begin >= tile.end) return;
+    const int in_slot = __builtin_amdgcn_readfirstlane(tile.sub);
+    const int a0 = in_slot / p.n_tiles * BA, n0 = in_slot % p.n_tiles * BN;
     const int group = __builtin_amdgcn_readfirstlane(tile.group);
 
     f32x4 acc[AT][NT];
@@ -61,7 +64,7 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
     const int wa = wave / WN, wn = wave % WN;
 
     // this lane's chunks of a stage: row within the stage, first kept index
-    constexpr int kALanes = BA * int(sizeof(T)) / 16, kBLanes = BN * int(sizeof(T)) / 16;
+    constexpr int kALanes = BA * int(sizeof(T)) / 16, kBLanes = LN * int(sizeof(T)) / 16;
     int ar[IA], ac[IA], br[IB], bc[IB];
 #pragma unroll
     for (int i = 0; i < IA; ++i) {
@@ -73,22 +76,32 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
     for (int i = 0; i < IB; ++i) {
         const int chunk = (wave * IB + i) * 64 + lane;
         br[i] = chunk / kBLanes;
-        bc[i] = n0 + ((chunk % kBLanes) ^ sum_swizzle<T, BN>(br[i])) * E;
+        const int c = ((chunk % kBLanes) ^ sum_swizzle<T, LN>(br[i])) * E;
+        bc[i] = c < BN ? n0 + c : p.n;
     }
-    const auto row_of = [&](int64_t pos) -> int64_t {
-        if (pos >= tile.end) return -1;
-        if (!p.perm) return pos;
-        const int64_t r = p.perm[pos];
-        return r >= 0 && r < p.n_rows ? r : -1;
+    const int rows = int(tile.end - tile.begin);
+    const int stages = (rows + BR - 1) / BR;
+    // rows of the stages from `first` on (a multiple of kIndexRows), -1 behind the end
+    const auto fill = [&](int first) {
+        for (int i = threadIdx.x; i < kIndexRows && first + i < stages * BR; i += kWaves * 64) {
+            int64_t r = -1;
+            if (first + i < rows) {
+                const int64_t pos = tile.begin + first + i;
+                r = p.perm ? p.perm[pos] : pos;
+                if (r < 0 || r >= p.n_rows) r = -1;
+            }
+            index[i] = int32_t(r);
+        }
     };
-    const auto load = [&](int64_t pos, char* buf) {
+    const auto load = [&](int stage, char* buf) {
+        const int at = stage * BR % kIndexRows;
 #pragma unroll
         for (int i = 0; i < IA; ++i) {
             char* to = buf + (wave * IA + i) * 1024;
-            const int64_t r = row_of(pos + ar[i]);
+            const int32_t r = index[at + ar[i]];
             const bool in = r >= 0 && ac[i] < p.k;
             const T* src = p.x + r * p.ldx + ac[i];
-            if constexpr (AV)
+            if constexpr (VEC)
                 load_to_lds(in ? static_cast<const void*>(src) : zero_chunk, lds_offset(to));
             else
                 *reinterpret_cast<u32x4*>(to + lane * 16) = load_partial(src, in ? p.k - ac[i] : 0);
@@ -96,44 +109,36 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
 #pragma unroll
         for (int i = 0; i < IB; ++i) {
             char* to = buf + kABytes + (wave * IB + i) * 1024;
-            const int64_t r = row_of(pos + br[i]);
+            const int32_t r = index[at + br[i]];
             const bool in = r >= 0 && bc[i] < p.n;
             const T* src = p.gy + r * p.ldg + bc[i];
-            if constexpr (BV)
+            if constexpr (VEC)
                 load_to_lds(in ? static_cast<const void*>(src) : zero_chunk, lds_offset(to));
             else
                 *reinterpret_cast<u32x4*>(to + lane * 16) = load_partial(src, in ? p.n - bc[i] : 0);
         }
     };
-    if (tile.begin < tile.end) {
-        load(tile.begin, lds);
-        wait_loads();
-        __syncthreads();
-        int cur = 0;
-        for (int64_t pos = tile.begin; pos < tile.end; pos += BR) {
-            const char* at = lds + cur * (kABytes + kBBytes);
-            cur ^= 1;
-            if (pos + BR < tile.end) load(pos + BR, lds + cur * (kABytes + kBBytes));
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                typename Frag<T>::V a[AT], b[NT];
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    b[j] = read_sum_frag<T, BN>(at + kABytes, wn * NT + j, s, lane);
-#pragma unroll
-                for (int i = 0; i < AT; ++i)
-                    a[i] = read_sum_frag<T, BA>(at, wa * AT + i, s, lane);
-#pragma unroll
-                for (int i = 0; i < AT; ++i)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) acc[i][j] = mma16(b[j], a[i], acc[i][j]);
-            }
-            wait_loads();
-            __syncthreads();
+    // a stage's loads, with the row indices they need in LDS
+    const auto issue = [&](int stage, char* buf) {
+        if (stage * BR % kIndexRows == 0) {
+            tile_barrier();   // every wavefront is done with the indices there
+            fill(stage * BR);
+            tile_barrier();
         }
-    }
+        load(stage, buf);
+    };
+    product_loop<T, AT, NT, KB, S, kBytes, IA + IB>(
+        stages, lds, acc, issue,
+        [&](const char* at, int i, int s) { return read_sum_frag<T, BA>(at, wa * AT + i, s, lane); },
+        [&](const char* at, int j, int s) {
+            return read_sum_frag<T, LN>(at + kABytes, wn * NT + j, s, lane);
+        });
 
     const bool whole = tile.tiles <= 1;   // the group's only piece
+    const bool wide = p.n % 4 == 0 && reinterpret_cast<uintptr_t>(p.gw) % 16 == 0;
+    // a cut group's pieces lie behind those of the groups before it: there are at
+    // most n_rows / piece + n_groups pieces, and group g's start at this one
+    const int64_t slot = start(group) / p.piece + group + tile.index;
     float* part = p.partial + slot * int64_t(p.k) * p.n;
     T* out = p.gw + group * int64_t(p.k) * p.n;
 #pragma unroll
@@ -144,6 +149,13 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
         for (int j = 0; j < NT; ++j) {
             const int n = n0 + (wn * NT + j) * 16 + 4 * (lane >> 4);
             const int64_t at = int64_t(a) * p.n + n;
+            if (wide && n + 4 <= p.n) {
+                if (whole)
+                    store4(out + at, acc[i][j]);
+                else
+                    store4(part + at, acc[i][j]);
+                continue;
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 if (n + q >= p.n) continue;
@@ -156,24 +168,71 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
     }
 }
 
-// Adds the partial sums of groups that were cut, in piece order.
+// Adds the partial sums of groups that were cut.  A workgroup takes 64 outputs;
+// each of its 16 rows of 16 lanes adds every 16th piece, four outputs a lane,
+// and the 16 sums are added in order.
 template <typename T>
 __global__ __launch_bounds__(256) void zs_wgrad_sum_kernel(const WgParams<T> p) {
+    __shared__ float sums[16][68];
     const int64_t kn = int64_t(p.k) * p.n;
     const int64_t g = blockIdx.y;
     const int64_t a = clamp_offset(p.offsets, g, p.n_rows),
                   b = clamp_offset(p.offsets, g + 1, p.n_rows);
     if (b - a <= p.piece) return;
-    const int64_t pieces = (b - a + p.piece - 1) / p.piece;
+    const int pieces = int((b - a + p.piece - 1) / p.piece);
     const float* from = p.partial + (a / p.piece + g) * kn;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < kn; i += int64_t(gridDim.x) * 256) {
-        float s = 0.0f;
-        for (int64_t j = 0; j < pieces; ++j) s += from[j * kn + i];
-        p.gw[g * kn + i] = T(s);
+    const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
+    const int64_t i = int64_t(blockIdx.x) * 64 + col * 4;
+    f32x4 s = {0, 0, 0, 0};
+    if (kn % 4 == 0 && i < kn) {
+#pragma unroll 4
+        for (int j = row; j < pieces; j += 16) s += *reinterpret_cast<const f32x4*>(from + j * kn + i);
+    } else {
+        for (int j = row; j < pieces; j += 16)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (i + q < kn) s[q] += from[j * kn + i + q];
+    }
+    *reinterpret_cast<f32x4*>(&sums[row][col * 4]) = s;
+    __syncthreads();
+    const int64_t o = int64_t(blockIdx.x) * 64 + threadIdx.x;
+    if (threadIdx.x < 64 && o < kn) {
+        float t = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) t += sums[r][threadIdx.x];
+        p.gw[g * kn + o] = T(t);
     }
 }
 
-constexpr int kBA = 128, kBN = 128;
+template <typename T, int BA, int BN, bool VEC>
+hipError_t run(WgParams<T> p, hipStream_t stream) {
+    constexpr int S = 2, KB = 128, BR = KB / sizeof(T);
+    p.k_tiles = (p.k + BA - 1) / BA, p.n_tiles = (p.n + BN - 1) / BN;
+    const int64_t slots = p.n_rows / p.piece + p.n_groups;
+    const int64_t grid = slots * p.k_tiles * p.n_tiles;
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    const int64_t longest = p.piece < p.n_rows ? p.piece : p.n_rows;
+    const int stages = int((longest + BR - 1) / BR);
+    const int bytes = (stages < 1 ? 1 : stages < S ? stages : S) * (BA + pow2_at_least(BN)) * KB;
+    auto* kernel = zs_wgrad_kernel<T, BA, BN, 2, 2, KB, S, VEC>;
+    if (bytes + 4 * kIndexRows > 65536) {
+        const hipError_t err = hipFuncSetAttribute(
+            reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (err != hipSuccess) return err;
+    }
+    kernel<<<dim3(unsigned(grid)), 256, bytes, stream>>>(p);
+    return hipGetLastError();
+}
+
+template <typename T, int BA>
+hipError_t by_n(const WgParams<T>& p, hipStream_t stream) {
+    switch (tile_side(p.n, true)) {
+        case 128: return run<T, BA, 128, true>(p, stream);
+        case 96: return run<T, BA, 96, true>(p, stream);
+        case 64: return run<T, BA, 64, true>(p, stream);
+        default: return run<T, BA, 32, true>(p, stream);
+    }
+}
 
 template <typename T>
 hipError_t dispatch(const WgradArgs& a, hipStream_t stream) {
@@ -181,33 +240,27 @@ hipError_t dispatch(const WgradArgs& a, hipStream_t stream) {
     const auto on16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     WgParams<T> p{static_cast<const T*>(a.x), static_cast<const T*>(a.gy), static_cast<T*>(a.gw),
                   a.partial, a.offsets, a.perm, a.ldx, a.ldg, a.n_rows, a.n_groups, a.piece,
-                  a.k, a.n, (a.k + kBA - 1) / kBA, (a.n + kBN - 1) / kBN};
-    const bool av = on16(a.x) && a.ldx % E == 0 && a.k % E == 0;
-    const bool bv = on16(a.gy) && a.ldg % E == 0 && a.n % E == 0;
-    const int64_t slots = a.n_rows / a.piece + a.n_groups;
-    const int64_t grid = slots * p.k_tiles * p.n_tiles;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    constexpr int bytes = 2 * (kBA + kBN) * kStageBytes;
-    const dim3 g{unsigned(grid)};
-    if (av && bv)
-        zs_wgrad_kernel<T, kBA, kBN, 2, 2, true, true><<<g, 256, bytes, stream>>>(p);
-    else if (av)
-        zs_wgrad_kernel<T, kBA, kBN, 2, 2, true, false><<<g, 256, bytes, stream>>>(p);
-    else if (bv)
-        zs_wgrad_kernel<T, kBA, kBN, 2, 2, false, true><<<g, 256, bytes, stream>>>(p);
+                  a.k, a.n, 0, 0};
+    const bool vec = on16(a.x) && a.ldx % E == 0 && a.k % E == 0 && on16(a.gy) && a.ldg % E == 0 &&
+                     a.n % E == 0;
+    hipError_t err;
+    if (!vec)
+        err = run<T, 64, 64, false>(p, stream);
+    else if (tile_side(a.k, false) == 128)
+        err = by_n<T, 128>(p, stream);
+    else if (tile_side(a.k, false) == 64)
+        err = by_n<T, 64>(p, stream);
     else
-        zs_wgrad_kernel<T, kBA, kBN, 2, 2, false, false><<<g, 256, bytes, stream>>>(p);
-    hipError_t err = hipGetLastError();
+        err = by_n<T, 32>(p, stream);
     if (err != hipSuccess || a.piece > a.n_rows) return err;
     const int64_t kn = int64_t(a.k) * a.n;
-    const int64_t bx = (kn + 255) / 256;
     for (int64_t g0 = 0; g0 < a.n_groups; g0 += 65535) {   // grid.y limit
         WgParams<T> q = p;
         q.offsets += g0;
         q.gw += g0 * kn;
         q.partial += g0 * kn;
         const int64_t ng = a.n_groups - g0 < 65535 ? a.n_groups - g0 : 65535;
-        zs_wgrad_sum_kernel<T><<<dim3(unsigned(bx < 4096 ? bx : 4096), unsigned(ng)), 256, 0, stream>>>(q);
+        zs_wgrad_sum_kernel<T><<<dim3(unsigned((kn + 63) / 64), unsigned(ng)), 256, 0, stream>>>(q);
         err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
@@ -217,7 +270,8 @@ hipError_t dispatch(const WgradArgs& a, hipStream_t stream) {
 }  // namespace
 
 WgradPlan plan_wgrad(int64_t n_rows, int64_t n_groups, int64_t k, int64_t n, bool bf16) {
-    const int64_t tiles = ((k + kBA - 1) / kBA) * ((n + kBN - 1) / kBN);
+    const int64_t ka = tile_side(k, false), nb = tile_side(n, true);
+    const int64_t tiles = ((k + ka - 1) / ka) * ((n + nb - 1) / nb);
     const int64_t step = bf16 ? 64 : 32;
     constexpr int64_t kWant = 1024, kLeast = 256;
     // enough groups and tiles to fill the GPU: no group is cut
