@@ -93,6 +93,37 @@ __device__ inline void load_param(const float* p, int chunk, int c, bool vec, fl
     }
 }
 
+// v of the lane that a DPP control picks within 16 lanes.
+template <int CTRL>
+__device__ inline float dpp(float v) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+// Sum over the L <= 64 lanes of a row, in all of them, without LDS: halves are
+// exchanged within 16 lanes by DPP (xor 1, xor 2, mirrors of 8 and 16 lanes),
+// then across 16 and 32 lanes by the permlane swaps, whose two results are the
+// two halves.
+template <int L>
+__device__ inline float lane_sum(float v) {
+    if constexpr (L >= 2) v += dpp<0xB1>(v);
+    if constexpr (L >= 4) v += dpp<0x4E>(v);
+    if constexpr (L >= 8) v += dpp<0x141>(v);
+    if constexpr (L >= 16) v += dpp<0x140>(v);
+    if constexpr (L >= 32) {
+        const int i = __builtin_bit_cast(int, v);
+        const auto r = __builtin_amdgcn_permlane16_swap(i, i, false, false);
+        const uint32_t a = r[0], b = r[1];
+        v = __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
+    }
+    if constexpr (L >= 64) {
+        const int i = __builtin_bit_cast(int, v);
+        const auto r = __builtin_amdgcn_permlane32_swap(i, i, false, false);
+        const uint32_t a = r[0], b = r[1];
+        v = __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
+    }
+    return v;
+}
+
 // Sums of N values over the L lanes of a row.  Above a wavefront the row is the
 // workgroup's and the wavefronts meet in LDS: `region` alternates, so that one
 // barrier per sum is enough (a region is written again only behind the next
@@ -100,9 +131,7 @@ __device__ inline void load_param(const float* p, int chunk, int c, bool vec, fl
 template <int L, int N>
 __device__ inline void row_sum(float (&v)[N], float* lds, int& region) {
 #pragma unroll
-    for (int h = (L < 64 ? L : 64) / 2; h >= 1; h >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], h, 64);
+    for (int i = 0; i < N; ++i) v[i] = lane_sum<(L < 64 ? L : 64)>(v[i]);
     if constexpr (L > 64) {
         constexpr int W = L / 64;
         float* at = lds + region * W * 2;
@@ -147,9 +176,31 @@ struct JoinParams {
     float *gscale, *gpost, *gpre, *partial;
 };
 
+// The calls that training makes (all inputs and outputs there, everything on 16
+// bytes) have code of their own without tests: a gate per channel, a gate per
+// row.  Any takes the rest by the parameters.  With the tests in the element
+// loops the gradients of 32768 x 2048 in bf16 took 291 us.
+enum Mode { kAny, kFull, kRow };
+template <Mode M, typename T>
+__device__ inline bool has_z(const JoinParams<T>& p) {
+    return M != kAny || p.z;
+}
+template <Mode M, typename T>
+__device__ inline bool has_pre(const JoinParams<T>& p) {
+    return M != kAny || p.w_pre;
+}
+template <Mode M, typename T>
+__device__ inline int gate_of(const JoinParams<T>& p) {
+    return M == kFull ? 2 : (M == kRow ? 1 : p.gate_kind);
+}
+template <Mode M, typename T>
+__device__ inline bool vec_of(const JoinParams<T>& p) {
+    return M != kAny || p.vec;
+}
+
 constexpr int threads_of(int L) { return L > 256 ? L : 256; }
 
-template <typename T, int L, int NV>
+template <typename T, int L, int NV, Mode M>
 __global__ __launch_bounds__(threads_of(L)) void zs_join_kernel(const JoinParams<T> p) {
     constexpr int V = Chunk<T>::V;
     constexpr int kRowsOf = threads_of(L) / L;
@@ -164,17 +215,17 @@ __global__ __launch_bounds__(threads_of(L)) void zs_join_kernel(const JoinParams
         float y[NV][V];
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            Chunk<T>::unpack(load_chunk(p.x + row * p.ldx, l + j * L, c, p.vec), y[j]);
-        if (p.z) {
+            Chunk<T>::unpack(load_chunk(p.x + row * p.ldx, l + j * L, c, vec_of<M>(p)), y[j]);
+        if (has_z<M>(p)) {
             u32x4 zr[NV], ar[NV];
             float row_gate = 0.0f;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) zr[j] = load_chunk(p.z + row * p.ldz, l + j * L, c, p.vec);
-            if (p.gate_kind == 2) {
+            for (int j = 0; j < NV; ++j) zr[j] = load_chunk(p.z + row * p.ldz, l + j * L, c, vec_of<M>(p));
+            if (gate_of<M>(p) == 2) {
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
-                    ar[j] = load_chunk(p.gate + row * p.ldg, l + j * L, c, p.vec);
-            } else if (p.gate_kind == 1 && live) {
+                    ar[j] = load_chunk(p.gate + row * p.ldg, l + j * L, c, vec_of<M>(p));
+            } else if (gate_of<M>(p) == 1 && live) {
                 row_gate = float(p.gate[row * p.ldg]);
             }
             float s[1] = {0.0f};
@@ -188,24 +239,24 @@ __global__ __launch_bounds__(threads_of(L)) void zs_join_kernel(const JoinParams
             row_sum<L>(s, lds, region);
             const float rz = 1.0f / sqrtf(__builtin_fmaf(s[0], p.inv_c, p.eps));
             float gate_s = 1.0f, gate_o = 0.0f;
-            if (p.gate_kind == 1) sigmoid2(row_gate, gate_s, gate_o);
+            if (gate_of<M>(p) == 1) sigmoid2(row_gate, gate_s, gate_o);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 float z[V], a[V], sc[V], wp[V];
                 Chunk<T>::unpack(zr[j], z);
-                load_param<V>(p.scale, l + j * L, c, p.vec, sc);
-                load_param<V>(p.w_post, l + j * L, c, p.vec, wp);
-                if (p.gate_kind == 2) Chunk<T>::unpack(ar[j], a);
+                load_param<V>(p.scale, l + j * L, c, vec_of<M>(p), sc);
+                load_param<V>(p.w_post, l + j * L, c, vec_of<M>(p), wp);
+                if (gate_of<M>(p) == 2) Chunk<T>::unpack(ar[j], a);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float g = gate_s, o;
-                    if (p.gate_kind == 2) sigmoid2(a[i], g, o);
+                    if (gate_of<M>(p) == 2) sigmoid2(a[i], g, o);
                     y[j][i] = __builtin_fmaf(sc[i] * g, z[i] * rz * wp[i], y[j][i]);
                 }
-                if (live) store_chunk(p.y + row * p.c, l + j * L, c, p.vec, Chunk<T>::pack(y[j]));
+                if (live) store_chunk(p.y + row * p.c, l + j * L, c, vec_of<M>(p), Chunk<T>::pack(y[j]));
             }
         }
-        if (p.w_pre) {
+        if (has_pre<M>(p)) {
             float s[1] = {0.0f};
 #pragma unroll
             for (int j = 0; j < NV; ++j)
@@ -216,17 +267,56 @@ __global__ __launch_bounds__(threads_of(L)) void zs_join_kernel(const JoinParams
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 float w[V];
-                load_param<V>(p.w_pre, l + j * L, c, p.vec, w);
+                load_param<V>(p.w_pre, l + j * L, c, vec_of<M>(p), w);
 #pragma unroll
                 for (int i = 0; i < V; ++i) w[i] = y[j][i] * ry * w[i];
-                if (live) store_chunk(p.h + row * p.c, l + j * L, c, p.vec, Chunk<T>::pack(w));
+                if (live) store_chunk(p.h + row * p.c, l + j * L, c, vec_of<M>(p), Chunk<T>::pack(w));
             }
         }
     }
 }
 
-template <typename T, int L, int NV>
-__global__ __launch_bounds__(threads_of(L)) void zs_join_bwd_kernel(const JoinParams<T> p) {
+// Workgroups of the backward on a compute unit: as many as the registers of a
+// lane's part of a row (and, with a gate per channel, its sigmoids) leave room
+// for without spilling.
+template <typename T, int L, int NV, Mode M>
+constexpr int resident() {
+    constexpr int held = NV * Chunk<T>::V;
+    if (L > 256) return 1;
+    return held <= 4 ? 4 : (held <= 8 || (held <= 12 && M == kRow) ? 3 : 2);
+}
+
+// A lane's part of a row's inputs as they lie in memory.
+template <int NV>
+struct RowInputs {
+    u32x4 z[NV], x[NV], gate[NV], gy[NV], gh[NV];
+    float row_gate;
+};
+template <typename T, int L, int NV, Mode M>
+__device__ inline RowInputs<NV> load_row(const JoinParams<T>& p, int64_t row, int l) {
+    RowInputs<NV> r;
+    const bool live = row < p.n_rows, vec = vec_of<M>(p);
+    const int c = live ? p.c : 0;
+    const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int at = l + j * L;
+        r.z[j] = r.x[j] = r.gate[j] = r.gy[j] = r.gh[j] = zero;
+        if (at * Chunk<T>::V < c) {
+            r.x[j] = load_chunk(p.x + row * p.ldx, at, c, vec);
+            if (has_z<M>(p)) r.z[j] = load_chunk(p.z + row * p.ldz, at, c, vec);
+            if (gate_of<M>(p) == 2) r.gate[j] = load_chunk(p.gate + row * p.ldg, at, c, vec);
+            if (M != kAny || p.gy) r.gy[j] = load_chunk(p.gy + row * p.c, at, c, vec);
+            if (M != kAny || p.gh) r.gh[j] = load_chunk(p.gh + row * p.c, at, c, vec);
+        }
+    }
+    r.row_gate = gate_of<M>(p) == 1 && live ? float(p.gate[row * p.ldg]) : 0.0f;
+    return r;
+}
+
+template <typename T, int L, int NV, Mode M>
+__global__ __launch_bounds__(threads_of(L), (resident<T, L, NV, M>())) void zs_join_bwd_kernel(
+    const JoinParams<T> p) {
     constexpr int V = Chunk<T>::V;
     constexpr int kThreads = threads_of(L), kRowsOf = kThreads / L;
     __shared__ float lds[2 * (L > 64 ? L / 64 : 1) * 2];
@@ -240,60 +330,56 @@ __global__ __launch_bounds__(threads_of(L)) void zs_join_bwd_kernel(const JoinPa
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[q][j][i] = 0.0f;
+    // a lane with one chunk of a row has registers left to load the next row's
+    // while this one's is used
+    constexpr bool kAhead = NV == 1;
+    RowInputs<NV> next;
+    if constexpr (kAhead) next = load_row<T, L, NV, M>(p, int64_t(blockIdx.x) * kRowsOf + slot, l);
     for (int64_t base = int64_t(blockIdx.x) * kRowsOf; base < p.n_rows;
          base += int64_t(gridDim.x) * kRowsOf) {
         const int64_t row = base + slot;
         const bool live = row < p.n_rows;
         const int c = live ? p.c : 0;
-        u32x4 zr[NV], ar[NV], yr[NV], hr[NV];
+        const RowInputs<NV> in = kAhead ? next : load_row<T, L, NV, M>(p, row, l);
+        if constexpr (kAhead) next = load_row<T, L, NV, M>(p, row + int64_t(gridDim.x) * kRowsOf, l);
         float y[NV][V];
-        float row_gate = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int at = l + j * L;
-            zr[j] = p.z ? load_chunk(p.z + row * p.ldz, at, c, p.vec) : u32x4{0, 0, 0, 0};
-            Chunk<T>::unpack(load_chunk(p.x + row * p.ldx, at, c, p.vec), y[j]);
-            ar[j] = p.gate_kind == 2 ? load_chunk(p.gate + row * p.ldg, at, c, p.vec)
-                                     : u32x4{0, 0, 0, 0};
-            yr[j] = p.gy ? load_chunk(p.gy + row * p.c, at, c, p.vec) : u32x4{0, 0, 0, 0};
-            hr[j] = p.gh ? load_chunk(p.gh + row * p.c, at, c, p.vec) : u32x4{0, 0, 0, 0};
-        }
-        if (p.gate_kind == 1 && live) row_gate = float(p.gate[row * p.ldg]);
+        for (int j = 0; j < NV; ++j) Chunk<T>::unpack(in.x[j], y[j]);
         float rz = 0.0f, gate_s = 1.0f, gate_o = 0.0f;
-        if (p.z) {
+        if (has_z<M>(p)) {
             float s[1] = {0.0f};
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 float z[V];
-                Chunk<T>::unpack(zr[j], z);
+                Chunk<T>::unpack(in.z[j], z);
 #pragma unroll
                 for (int i = 0; i < V; ++i) s[0] = __builtin_fmaf(z[i], z[i], s[0]);
             }
             row_sum<L>(s, lds, region);
             rz = 1.0f / sqrtf(__builtin_fmaf(s[0], p.inv_c, p.eps));
-            if (p.gate_kind == 1) sigmoid2(row_gate, gate_s, gate_o);
+            if (gate_of<M>(p) == 1) sigmoid2(in.row_gate, gate_s, gate_o);
         }
         float s2[2] = {0.0f, 0.0f};   // y^2, t y
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int at = l + j * L;
-            if (p.z) {
+            if (has_z<M>(p)) {
                 float z[V], a[V], sc[V], wp[V];
-                Chunk<T>::unpack(zr[j], z);
-                load_param<V>(p.scale, at, c, p.vec, sc);
-                load_param<V>(p.w_post, at, c, p.vec, wp);
-                if (p.gate_kind == 2) Chunk<T>::unpack(ar[j], a);
+                Chunk<T>::unpack(in.z[j], z);
+                load_param<V>(p.scale, at, c, vec_of<M>(p), sc);
+                load_param<V>(p.w_post, at, c, vec_of<M>(p), wp);
+                if (gate_of<M>(p) == 2) Chunk<T>::unpack(in.gate[j], a);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float g = gate_s, o;
-                    if (p.gate_kind == 2) sigmoid2(a[i], g, o);
+                    if (gate_of<M>(p) == 2) sigmoid2(a[i], g, o);
                     y[j][i] = __builtin_fmaf(sc[i] * g, z[i] * rz * wp[i], y[j][i]);
                 }
             }
-            if (p.w_pre) {
+            if (has_pre<M>(p)) {
                 float gh[V], w[V];
-                Chunk<T>::unpack(hr[j], gh);
-                load_param<V>(p.w_pre, at, c, p.vec, w);
+                Chunk<T>::unpack(in.gh[j], gh);
+                load_param<V>(p.w_pre, at, c, vec_of<M>(p), w);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     s2[0] = __builtin_fmaf(y[j][i], y[j][i], s2[0]);
@@ -302,7 +388,7 @@ __global__ __launch_bounds__(threads_of(L)) void zs_join_bwd_kernel(const JoinPa
             }
         }
         float ry = 0.0f, my = 0.0f;   // my = ry^3 mean(t y)
-        if (p.w_pre) {
+        if (has_pre<M>(p)) {
             row_sum<L>(s2, lds, region);
             ry = 1.0f / sqrtf(__builtin_fmaf(s2[0], p.inv_c, p.eps));
             my = ry * ry * ry * (s2[1] * p.inv_c);
@@ -312,28 +398,28 @@ __global__ __launch_bounds__(threads_of(L)) void zs_join_bwd_kernel(const JoinPa
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int at = l + j * L;
-            Chunk<T>::unpack(yr[j], gx[j]);
-            if (p.w_pre) {
+            Chunk<T>::unpack(in.gy[j], gx[j]);
+            if (has_pre<M>(p)) {
                 float gh[V], w[V];
-                Chunk<T>::unpack(hr[j], gh);
-                load_param<V>(p.w_pre, at, c, p.vec, w);
+                Chunk<T>::unpack(in.gh[j], gh);
+                load_param<V>(p.w_pre, at, c, vec_of<M>(p), w);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     acc[2][j][i] = __builtin_fmaf(gh[i] * ry, y[j][i], acc[2][j][i]);
                     gx[j][i] = __builtin_fmaf(ry, gh[i] * w[i], gx[j][i]) - my * y[j][i];
                 }
             }
-            if (live) store_chunk(p.gx + row * p.c, at, c, p.vec, Chunk<T>::pack(gx[j]));
-            if (p.z) {
+            if (live) store_chunk(p.gx + row * p.c, at, c, vec_of<M>(p), Chunk<T>::pack(gx[j]));
+            if (has_z<M>(p)) {
                 float z[V], a[V], sc[V], wp[V], ga[V];
-                Chunk<T>::unpack(zr[j], z);
-                load_param<V>(p.scale, at, c, p.vec, sc);
-                load_param<V>(p.w_post, at, c, p.vec, wp);
-                if (p.gate_kind == 2) Chunk<T>::unpack(ar[j], a);
+                Chunk<T>::unpack(in.z[j], z);
+                load_param<V>(p.scale, at, c, vec_of<M>(p), sc);
+                load_param<V>(p.w_post, at, c, vec_of<M>(p), wp);
+                if (gate_of<M>(p) == 2) Chunk<T>::unpack(in.gate[j], a);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float g = gate_s, o = gate_o;
-                    if (p.gate_kind == 2) sigmoid2(a[i], g, o);
+                    if (gate_of<M>(p) == 2) sigmoid2(a[i], g, o);
                     const float zn = z[i] * rz, u = zn * wp[i];
                     const float b = gx[j][i] * g, q = b * sc[i], r = q * wp[i];
                     acc[0][j][i] = __builtin_fmaf(b, u, acc[0][j][i]);
@@ -343,21 +429,21 @@ __global__ __launch_bounds__(threads_of(L)) void zs_join_bwd_kernel(const JoinPa
                     s3[1] += ga[i];
                     gx[j][i] = r;
                 }
-                if (p.gate_kind == 2 && live)
-                    store_chunk(p.ggate + row * p.c, at, c, p.vec, Chunk<T>::pack(ga));
+                if (gate_of<M>(p) == 2 && live)
+                    store_chunk(p.ggate + row * p.c, at, c, vec_of<M>(p), Chunk<T>::pack(ga));
             }
         }
-        if (p.z) {
+        if (has_z<M>(p)) {
             row_sum<L>(s3, lds, region);
-            if (p.gate_kind == 1 && live && l == 0) p.ggate[row] = T(s3[1]);
+            if (gate_of<M>(p) == 1 && live && l == 0) p.ggate[row] = T(s3[1]);
             const float mz = s3[0] * p.inv_c;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 float z[V];
-                Chunk<T>::unpack(zr[j], z);
+                Chunk<T>::unpack(in.z[j], z);
 #pragma unroll
                 for (int i = 0; i < V; ++i) z[i] = rz * (gx[j][i] - z[i] * rz * mz);
-                if (live) store_chunk(p.gz + row * p.c, l + j * L, c, p.vec, Chunk<T>::pack(z));
+                if (live) store_chunk(p.gz + row * p.c, l + j * L, c, vec_of<M>(p), Chunk<T>::pack(z));
             }
         }
     }
@@ -439,31 +525,42 @@ JoinParams<T> params(const JoinArgs& a) {
 
 constexpr int64_t kMaxPartials = 1024;
 
-template <typename T, int L, int NV>
-hipError_t run(const JoinArgs& a, bool backward, hipStream_t stream) {
-    const JoinParams<T> p = params<T>(a);
+template <typename T, int L, int NV, Mode M>
+hipError_t run_mode(const JoinParams<T>& p, bool backward, hipStream_t stream) {
     constexpr int rows = threads_of(L) / L;
-    const int64_t want = (a.n_rows + rows - 1) / rows;
+    const int64_t want = (p.n_rows + rows - 1) / rows;
     if (!backward) {
         const unsigned grid = unsigned(want < 8192 ? want : 8192);
-        zs_join_kernel<T, L, NV><<<grid, threads_of(L), 0, stream>>>(p);
+        zs_join_kernel<T, L, NV, M><<<grid, threads_of(L), 0, stream>>>(p);
         return hipGetLastError();
     }
-    const int64_t cap = join_workspace(a.n_rows, a.c) / (12 * int64_t(a.c));
+    // one round of workgroups that all run at once
+    constexpr int64_t cap = 256 * resident<T, L, NV, M>();
+    static_assert(cap <= kMaxPartials, "partial sums for every workgroup");
     const unsigned grid = unsigned(want < cap ? want : cap);
     if (grid > 0) {
-        zs_join_bwd_kernel<T, L, NV><<<grid, threads_of(L), 0, stream>>>(p);
+        zs_join_bwd_kernel<T, L, NV, M><<<grid, threads_of(L), 0, stream>>>(p);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
-    zs_join_sum_kernel<<<(3 * a.c + 31) / 32, 1024, 0, stream>>>(a.partial, int(grid), a.c,
-                                                                 a.gscale, a.gpost, a.gpre);
+    zs_join_sum_kernel<<<(3 * p.c + 31) / 32, 1024, 0, stream>>>(p.partial, int(grid), p.c,
+                                                                 p.gscale, p.gpost, p.gpre);
     return hipGetLastError();
 }
 
+template <typename T, int L, int NV>
+hipError_t run(const JoinArgs& a, bool backward, hipStream_t stream) {
+    const JoinParams<T> p = params<T>(a);
+    const bool all = p.vec && p.z && p.w_pre && (!backward || (p.gy && p.gh));
+    if (all && p.gate_kind == 2) return run_mode<T, L, NV, kFull>(p, backward, stream);
+    if (all && p.gate_kind == 1) return run_mode<T, L, NV, kRow>(p, backward, stream);
+    return run_mode<T, L, NV, kAny>(p, backward, stream);
+}
+
 // Lanes and chunks per lane by the row's width in chunks: the fewest lanes that
-// hold a row in one chunk each up to a wavefront, then up to four chunks a lane
-// of a wavefront, then a workgroup.
+// hold a row in one chunk each up to a wavefront, then two or three chunks a
+// lane, then a workgroup (bf16 chunks are eight values: three of them a lane
+// spill in the backward).
 template <typename T>
 hipError_t dispatch(const JoinArgs& a, bool backward, hipStream_t stream) {
     const int chunks = (a.c + Chunk<T>::V - 1) / Chunk<T>::V;
@@ -475,12 +572,17 @@ hipError_t dispatch(const JoinArgs& a, bool backward, hipStream_t stream) {
     if (chunks <= 32) return run<T, 32, 1>(a, backward, stream);
     if (chunks <= 64) return run<T, 64, 1>(a, backward, stream);
     if (chunks <= 128) return run<T, 64, 2>(a, backward, stream);
-    if (chunks <= 192) return run<T, 64, 3>(a, backward, stream);
-    if (chunks <= 256) return run<T, 256, 1>(a, backward, stream);
-    if (chunks <= 512) return run<T, 256, 2>(a, backward, stream);
-    if (chunks <= 1024) return run<T, 256, 4>(a, backward, stream);
-    if constexpr (sizeof(T) == 4) return run<T, 1024, 2>(a, backward, stream);
-    return hipErrorInvalidValue;   // wider than ZS_MAX_JOIN_WIDTH: refused before
+    if constexpr (sizeof(T) == 4) {
+        if (chunks <= 192) return run<T, 64, 3>(a, backward, stream);
+        if (chunks <= 256) return run<T, 256, 1>(a, backward, stream);
+        if (chunks <= 512) return run<T, 256, 2>(a, backward, stream);
+        if (chunks <= 1024) return run<T, 256, 4>(a, backward, stream);
+        return run<T, 512, 4>(a, backward, stream);
+    } else {
+        if (chunks <= 256) return run<T, 256, 1>(a, backward, stream);
+        if (chunks <= 512) return run<T, 256, 2>(a, backward, stream);
+        return run<T, 512, 2>(a, backward, stream);
+    }
 }
 
 }  // namespace

@@ -174,75 +174,45 @@ __device__ inline void store4(T* p, f32x4 v) {
 
 // The product loop over `stages` stages, S buffers of kBytes deep.  issue(i, buf)
 // starts the loads of stage i (kLoads per wavefront); read_a(buf, i, s) and
-// read_b(buf, j, s) read fragments of sub-stage s.
-//
-// Fragments are read ahead of the matrix instructions that use them: the b of
-// the next sub-stage and A row fragments up to `ahead` rows on, so that the
-// LDS works while the matrix cores do; read together behind the barrier the two
-// took turns (256 x 256 tiles in bf16 kept the matrix cores busy 53 % of the
-// time).  The barrier of a new stage therefore comes `ahead` rows before the end
-// of the old one, when the last of its fragments have been read; its buffer is
-// then free for stage i + S.  Behind the last stage the reads ahead fetch
-// values that nothing uses, from the workgroup's own buffers.
+// read_b(buf, j, s) read fragments of sub-stage s.  One barrier a stage: it
+// publishes the stage and says that every wavefront is done with the one before,
+// whose buffer the next loads fill.  (Reading the fragments of the next sub-stage
+// ahead, across the barrier, was no faster in the products and slower in the
+// weight gradient, whose transposed reads then crowd its registers: 16384 x
+// 4096 x 4096 in bf16 495 us either way, its weight gradient 680 and 775.)
 template <typename T, int MT, int NT, int KB, int S, int kBytes, int kLoads, typename Issue,
           typename ReadA, typename ReadB>
 __device__ inline void product_loop(int stages, char* lds, f32x4 (&acc)[MT][NT], Issue issue,
                                     ReadA read_a, ReadB read_b) {
     using V = typename Frag<T>::V;
-    constexpr int NS = KB / 64, ahead = MT < 4 ? MT : 4;
+    constexpr int NS = KB / 64;
     if (stages <= 0) return;
 #pragma unroll
-    for (int i = 0; i < S; ++i)
+    for (int i = 0; i < S - 1; ++i)
         if (i < stages) issue(i, lds + i * kBytes);
-    if (stages >= S)
-        wait_loads<(S - 1) * kLoads>();
-    else
-        wait_loads<0>();
-    tile_barrier();
-    V a[MT], b[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) b[j] = read_b(lds, j, 0);
-#pragma unroll
-    for (int i = 0; i < ahead; ++i) a[i] = read_a(lds, i, 0);
     int cur = 0;
     for (int stage = 0; stage < stages; ++stage) {
-        char* at = lds + cur * kBytes;
-        const int next = cur + 1 == S ? 0 : cur + 1;
-        // one buffer only: there is one stage
-        char* behind = stages > next ? lds + next * kBytes : lds;
+        // `stage` has arrived when at most the S - 2 stages behind it are in flight
+        if (stage + S - 1 <= stages)
+            wait_loads<(S - 2) * kLoads>();
+        else
+            wait_loads<0>();
+        tile_barrier();
+        const char* at = lds + cur * kBytes;
+        if (stage + S - 1 < stages) issue(stage + S - 1, lds + (cur == 0 ? S - 1 : cur - 1) * kBytes);
+        cur = cur + 1 == S ? 0 : cur + 1;
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-            const char* from = at;
-            V b_next[NT], a_next[ahead];
+            V a[MT], b[NT];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                if (i == MT - ahead) {
-                    if (s == NS - 1) {
-                        // stage + 1 has arrived when at most the S - 2 behind it are in flight
-                        if (stage + S <= stages)
-                            wait_loads<(S - 2) * kLoads>();
-                        else
-                            wait_loads<0>();
-                        tile_barrier();
-                        if (stage + S < stages) issue(stage + S, at);
-                        from = behind;
-                    }
+            for (int j = 0; j < NT; ++j) b[j] = read_b(at, j, s);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) b_next[j] = read_b(from, j, (s + 1) % NS);
-                }
-                if (i + ahead < MT)
-                    a[i + ahead] = read_a(at, i + ahead, s);
-                else
-                    a_next[i + ahead - MT] = read_a(from, i + ahead - MT, (s + 1) % NS);
+            for (int i = 0; i < MT; ++i) a[i] = read_a(at, i, s);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int j = 0; j < NT; ++j) acc[i][j] = mma16(b[j], a[i], acc[i][j]);
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j) b[j] = b_next[j];
-#pragma unroll
-            for (int i = 0; i < ahead; ++i) a[i] = a_next[i];
         }
-        cur = next;
     }
 }
 
@@ -283,66 +253,95 @@ __device__ inline TileOf tile_at(int64_t v, int64_t index, int64_t step, int64_t
 // Up to this many groups a wavefront adds up all groups' tiles, 64 at a time.
 constexpr int kCountedGroups = 512;
 
+// Workgroups for at most `items` work items: find_work gives an XCD an eighth of
+// each of two kinds, both rounded up.
+inline int64_t work_grid(int64_t items) { return items + 16; }
+
+// Inclusive sum over the wavefront's lanes.
+__device__ inline uint32_t lane_scan(uint32_t n, int lane) {
+#pragma unroll
+    for (int h = 1; h < 64; h <<= 1) {
+        const uint32_t o = __shfl_up(n, h, 64);
+        if (lane >= h) n += o;
+    }
+    return n;
+}
+
 // The work of workgroup `id`: start(v), v = 0 .. count, are the groups' clamped
-// boundaries; a group has a tile for each `step` of its rows, `least` at least,
-// and a tile `subs` work items.  Workgroups go to the 8 XCDs in turn, so XCD x,
-// which holds the ids x, x + 8, ..., gets an eighth of the items, in one piece:
-// neighbouring items share its L2, and no XCD has more tiles than another
-// (dealing out the ids of the second scheme, whose empty ones fall anywhere,
-// left some XCDs a tile more than they have room for at a time: 16384 rows of
-// 8 equal groups, 512 -> 512 in fp32, took 113 us instead of 83).
+// boundaries; group v has a tile for each `step` of its rows, least(v) at least,
+// and a tile `subs` work items.
+//
+// Workgroups go to the 8 XCDs in turn, so XCD x, which holds the ids x, x + 8,
+// ..., gets an eighth of the full tiles' items and then an eighth of the
+// part-filled tiles', each in one piece: neighbouring items share its L2, no XCD
+// has more to do than another, and what is dispatched last is short.  (Dealing
+// out the ids of the second scheme, whose empty ones fall anywhere, left some
+// XCDs a tile more than they have room for at a time: 16384 rows of 8 equal
+// groups, 512 -> 512 in fp32, took 113 us instead of 83.)
 //
 // With more groups, group v owns the slots from start(v) / step + v up to the
 // next group's: never fewer than its tiles, increasing with v, and a search over
 // the boundaries, 64 probes at a time, finds a slot's group.
-template <typename Start>
+template <typename Start, typename Least>
 __device__ inline TileOf find_work(uint32_t id, uint32_t grid, int subs, int64_t count,
-                                   int64_t step, int least, Start start) {
+                                   int64_t step, Start start, Least least) {
     const int lane = threadIdx.x & 63;
     TileOf none{};
     none.group = -1;
-    const uint32_t xcd = id % 8, nth = id / 8;
+    const uint32_t xcd = id % 8;
+    uint32_t nth = id / 8;
     if (count <= kCountedGroups) {
-        uint32_t before[kCountedGroups / 64], total = 0;   // inclusive, per lane; of all
+        constexpr int kChunks = kCountedGroups / 64;
         const int chunks = int((count + 63) / 64);
+        // full tiles and part-filled ones of this lane's groups, summed up to it
+        uint32_t before[2][kChunks], total[2] = {0, 0};
 #pragma unroll
-        for (int c = 0; c < kCountedGroups / 64; ++c) {
-            before[c] = 0;
+        for (int c = 0; c < kChunks; ++c) {
+            before[0][c] = before[1][c] = 0;
             if (c >= chunks) continue;
             const int64_t v = c * 64 + lane;
-            uint32_t n = 0;
+            uint32_t full = 0, part = 0;
             if (v < count) {
                 const int64_t a = start(v), b = start(v + 1);
-                n = b > a ? (uint32_t(b - a) + uint32_t(step) - 1) / uint32_t(step) : 0;
-                n = n < uint32_t(least) ? uint32_t(least) : n;
+                const uint32_t rows = b > a ? uint32_t(b - a) : 0;
+                full = rows / uint32_t(step);
+                part = full * uint32_t(step) < rows || (rows == 0 && least(v) > 0) ? 1 : 0;
             }
-#pragma unroll
-            for (int h = 1; h < 64; h <<= 1) {
-                const uint32_t o = __shfl_up(n, h, 64);
-                if (lane >= h) n += o;
-            }
-            before[c] = total + n;
-            total = __builtin_amdgcn_readlane(before[c], 63);
+            before[0][c] = total[0] + lane_scan(full, lane);
+            before[1][c] = total[1] + lane_scan(part, lane);
+            total[0] = __builtin_amdgcn_readlane(before[0][c], 63);
+            total[1] = __builtin_amdgcn_readlane(before[1][c], 63);
         }
-        const uint64_t items = uint64_t(total) * uint32_t(subs);
-        const uint64_t per = items / 8, rest = items % 8;
-        if (nth >= per + (xcd < rest ? 1 : 0)) return none;
-        const uint64_t item = xcd * per + (xcd < rest ? xcd : rest) + nth;
-        const uint32_t tile = uint32_t(item / uint32_t(subs));
-        uint32_t base = 0;
 #pragma unroll
-        for (int c = 0; c < kCountedGroups / 64; ++c) {
-            if (c >= chunks) continue;
-            const uint32_t last = __builtin_amdgcn_readlane(before[c], 63);
-            if (tile < last) {
-                const int l = __popcll(__ballot(before[c] <= tile));   // lanes before the group
-                const uint32_t first = l > 0 ? uint32_t(__shfl(before[c], l - 1, 64)) : base;
-                const int64_t v = c * 64 + l;
-                TileOf t = tile_at(v, tile - first, step, start(v), start(v + 1));
-                t.sub = int(item - uint64_t(tile) * uint32_t(subs));
-                return t;
+        for (int k = 0; k < 2; ++k) {
+            const uint64_t items = uint64_t(total[k]) * uint32_t(subs);
+            const uint64_t per = items / 8, rest = items % 8;
+            const uint32_t mine = uint32_t(per) + (xcd < rest ? 1 : 0);
+            if (nth >= mine) {
+                nth -= mine;
+                continue;
             }
-            base = last;
+            const uint64_t item = xcd * per + (xcd < rest ? xcd : rest) + nth;
+            const uint32_t tile = uint32_t(item / uint32_t(subs));
+            uint32_t base = 0;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                if (c >= chunks) continue;
+                const uint32_t last = __builtin_amdgcn_readlane(before[k][c], 63);
+                if (tile < last) {
+                    // lanes whose groups lie before the tile's
+                    const int l = __popcll(__ballot(before[k][c] <= tile));
+                    const uint32_t first =
+                        l > 0 ? uint32_t(__shfl(before[k][c], l - 1, 64)) : base;
+                    const int64_t v = c * 64 + l, a = start(v), b = start(v + 1);
+                    const uint32_t index =
+                        k == 0 ? tile - first : (b > a ? uint32_t(b - a) / uint32_t(step) : 0);
+                    TileOf t = tile_at(v, index, step, a, b);
+                    t.sub = int(item - uint64_t(tile) * uint32_t(subs));
+                    return t;
+                }
+                base = last;
+            }
         }
         return none;
     }
@@ -363,7 +362,7 @@ __device__ inline TileOf find_work(uint32_t id, uint32_t grid, int subs, int64_t
     const int64_t index = slot - (uint32_t(a) / uint32_t(step) + lo);
     if (index < 0) return none;
     TileOf t = tile_at(lo, index, step, a, start(lo + 1));
-    if (index >= (t.tiles > least ? t.tiles : least)) return none;
+    if (index >= (t.tiles > 0 ? t.tiles : least(lo))) return none;
     t.sub = int(item - uint32_t(slot) * uint32_t(subs));
     return t;
 }

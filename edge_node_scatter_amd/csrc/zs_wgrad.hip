@@ -30,6 +30,12 @@ __device__ inline int64_t clamp_offset(const int32_t* offsets, int64_t v, int64_
     return o < 0 ? 0 : (o > n_rows ? n_rows : o);
 }
 
+// Where the partial sums of a cut group that starts at position `start` begin: a
+// group of c > piece rows has ceil(c / piece) <= floor(2 c / piece) pieces, and
+// floor(2 (a + c) / piece) >= floor(2 a / piece) + floor(2 c / piece), so the
+// pieces of cut groups never meet and end by floor(2 n_rows / piece).
+__device__ inline int64_t first_piece(int64_t start, int64_t piece) { return 2 * start / piece; }
+
 constexpr int pow2_at_least(int v) { return v <= 32 ? 32 : v <= 64 ? 64 : 128; }
 constexpr int kIndexRows = 1024;   // row indices kept in LDS at a time
 
@@ -50,7 +56,7 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const auto start = [&](int64_t v) { return clamp_offset(p.offsets, v, p.n_rows); };
     const TileOf tile = find_work(blockIdx.x, gridDim.x, p.k_tiles * p.n_tiles, p.n_groups,
-                                  p.piece, 1, start);
+                                  p.piece, start, [](int64_t) { return 1; });
     if (tile.group < 0) return;
     const int in_slot = __builtin_amdgcn_readfirstlane(tile.sub);
     const int a0 = in_slot / p.n_tiles * BA, n0 = in_slot % p.n_tiles * BN;
@@ -136,9 +142,7 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
 
     const bool whole = tile.tiles <= 1;   // the group's only piece
     const bool wide = p.n % 4 == 0 && reinterpret_cast<uintptr_t>(p.gw) % 16 == 0;
-    // a cut group's pieces lie behind those of the groups before it: there are at
-    // most n_rows / piece + n_groups pieces, and group g's start at this one
-    const int64_t slot = start(group) / p.piece + group + tile.index;
+    const int64_t slot = first_piece(start(group), p.piece) + tile.index;
     float* part = p.partial + slot * int64_t(p.k) * p.n;
     T* out = p.gw + group * int64_t(p.k) * p.n;
 #pragma unroll
@@ -168,9 +172,14 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
     }
 }
 
-// Adds the partial sums of groups that were cut.  A workgroup takes 64 outputs;
-// each of its 16 rows of 16 lanes adds every 16th piece, four outputs a lane,
-// and the 16 sums are added in order.
+// Adds the partial sums of groups that were cut.  Up to 16 pieces: each thread
+// adds them for four outputs of its own.  More: 64 outputs at a time, each of a
+// workgroup's 16 rows of 16 lanes adds every 16th piece, four outputs a lane, and
+// the 16 sums are added in order.  Few workgroups a group (kSumBlocks), because
+// those of groups that were not cut have nothing to do: one for every 64 outputs
+// of 16 groups of 776 x 1160 took 63 us, nearly all of it to start them.
+constexpr int kSumBlocks = 256;
+
 template <typename T>
 __global__ __launch_bounds__(256) void zs_wgrad_sum_kernel(const WgParams<T> p) {
     __shared__ float sums[16][68];
@@ -180,27 +189,48 @@ __global__ __launch_bounds__(256) void zs_wgrad_sum_kernel(const WgParams<T> p) 
                   b = clamp_offset(p.offsets, g + 1, p.n_rows);
     if (b - a <= p.piece) return;
     const int pieces = int((b - a + p.piece - 1) / p.piece);
-    const float* from = p.partial + (a / p.piece + g) * kn;
-    const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
-    const int64_t i = int64_t(blockIdx.x) * 64 + col * 4;
-    f32x4 s = {0, 0, 0, 0};
-    if (kn % 4 == 0 && i < kn) {
+    const float* from = p.partial + first_piece(a, p.piece) * kn;
+    T* out = p.gw + g * kn;
+    if (pieces <= 16 && kn % 4 == 0) {
+        const bool wide = reinterpret_cast<uintptr_t>(p.gw) % 16 == 0;
+        for (int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4; i < kn;
+             i += int64_t(gridDim.x) * 1024) {
+            f32x4 s = {0, 0, 0, 0};
 #pragma unroll 4
-        for (int j = row; j < pieces; j += 16) s += *reinterpret_cast<const f32x4*>(from + j * kn + i);
-    } else {
-        for (int j = row; j < pieces; j += 16)
+            for (int j = 0; j < pieces; ++j)
+                s += *reinterpret_cast<const f32x4*>(from + j * kn + i);
+            if (wide)
+                store4(out + i, s);
+            else
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (i + q < kn) s[q] += from[j * kn + i + q];
+                for (int q = 0; q < 4; ++q) out[i + q] = T(s[q]);
+        }
+        return;
     }
-    *reinterpret_cast<f32x4*>(&sums[row][col * 4]) = s;
-    __syncthreads();
-    const int64_t o = int64_t(blockIdx.x) * 64 + threadIdx.x;
-    if (threadIdx.x < 64 && o < kn) {
-        float t = 0.0f;
+    const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
+    for (int64_t first = int64_t(blockIdx.x) * 64; first < kn; first += int64_t(gridDim.x) * 64) {
+        const int64_t i = first + col * 4;
+        f32x4 s = {0, 0, 0, 0};
+        if (kn % 4 == 0 && i < kn) {
+#pragma unroll 4
+            for (int j = row; j < pieces; j += 16)
+                s += *reinterpret_cast<const f32x4*>(from + j * kn + i);
+        } else {
+            for (int j = row; j < pieces; j += 16)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) t += sums[r][threadIdx.x];
-        p.gw[g * kn + o] = T(t);
+                for (int q = 0; q < 4; ++q)
+                    if (i + q < kn) s[q] += from[j * kn + i + q];
+        }
+        *reinterpret_cast<f32x4*>(&sums[row][col * 4]) = s;
+        __syncthreads();
+        const int64_t o = first + threadIdx.x;
+        if (threadIdx.x < 64 && o < kn) {
+            float t = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) t += sums[r][threadIdx.x];
+            out[o] = T(t);
+        }
+        __syncthreads();
     }
 }
 
@@ -209,7 +239,7 @@ hipError_t run(WgParams<T> p, hipStream_t stream) {
     constexpr int S = 2, KB = 128, BR = KB / sizeof(T);
     p.k_tiles = (p.k + BA - 1) / BA, p.n_tiles = (p.n + BN - 1) / BN;
     const int64_t slots = p.n_rows / p.piece + p.n_groups;
-    const int64_t grid = slots * p.k_tiles * p.n_tiles;
+    const int64_t grid = work_grid(slots * p.k_tiles * p.n_tiles);
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     const int64_t longest = p.piece < p.n_rows ? p.piece : p.n_rows;
     const int stages = int((longest + BR - 1) / BR);
@@ -258,9 +288,10 @@ hipError_t dispatch(const WgradArgs& a, hipStream_t stream) {
         WgParams<T> q = p;
         q.offsets += g0;
         q.gw += g0 * kn;
-        q.partial += g0 * kn;
         const int64_t ng = a.n_groups - g0 < 65535 ? a.n_groups - g0 : 65535;
-        zs_wgrad_sum_kernel<T><<<dim3(unsigned((kn + 63) / 64), unsigned(ng)), 256, 0, stream>>>(q);
+        const int64_t bx = (kn + 63) / 64;
+        zs_wgrad_sum_kernel<T><<<dim3(unsigned(bx < kSumBlocks ? bx : kSumBlocks), unsigned(ng)),
+                                 256, 0, stream>>>(q);
         err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
@@ -272,15 +303,16 @@ hipError_t dispatch(const WgradArgs& a, hipStream_t stream) {
 WgradPlan plan_wgrad(int64_t n_rows, int64_t n_groups, int64_t k, int64_t n, bool bf16) {
     const int64_t ka = tile_side(k, false), nb = tile_side(n, true);
     const int64_t tiles = ((k + ka - 1) / ka) * ((n + nb - 1) / nb);
-    const int64_t step = bf16 ? 64 : 32;
-    constexpr int64_t kWant = 1024, kLeast = 256;
-    // enough groups and tiles to fill the GPU: no group is cut
-    if (n_groups * tiles >= kWant || n_rows <= kLeast) return WgradPlan{n_rows + 1, 0};
-    int64_t piece = (n_rows * tiles / kWant + step - 1) / step * step;
-    if (piece < kLeast) piece = kLeast;
-    if (piece > n_rows) return WgradPlan{n_rows + 1, 0};
-    const int64_t slots = n_rows / piece + n_groups;
-    return WgradPlan{piece, size_t(slots * k * n * 4)};
+    // One round of workgroups: rows x tiles spread evenly over as many as run at
+    // once (LDS for two stages each, 160 KiB a compute unit).  Shorter pieces cost
+    // more partial sums (a tile in fp32, written and read), longer ones leave
+    // compute units idle behind the longest group.
+    const int64_t lds = 2 * (ka + pow2_at_least(int(nb))) * 128 + 4 * kIndexRows;
+    const int64_t want = 256 * (163840 / lds), step = bf16 ? 64 : 32;
+    int64_t piece = (n_rows * tiles / want + step - 1) / step * step;
+    if (piece < 256) piece = 256;
+    if (piece >= n_rows) return WgradPlan{n_rows + 1, 0};
+    return WgradPlan{piece, size_t((2 * n_rows / piece + 1) * k * n * 4)};
 }
 
 hipError_t launch_wgrad(const WgradArgs& a, bool bf16, hipStream_t stream) {
