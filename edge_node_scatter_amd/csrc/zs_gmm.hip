@@ -49,7 +49,7 @@ __global__ __launch_bounds__(WM * WN * 64) void zs_gmm_kernel(const MmParams<T> 
         const int64_t o = p.offsets[v - 1];
         return o < 0 ? 0 : (o > p.n_rows ? p.n_rows : o);
     };
-    const TileOf tile = find_work(blockIdx.x, gridDim.x, p.n_tiles, p.n_groups + 2, BM, start,
+    const TileOf tile = find_work(blockIdx.x, gridDim.x, p.n_tiles, false, p.n_groups + 2, BM, start,
                                   [](int64_t) { return 0; });
     if (tile.group < 0) return;
     const int n0 = __builtin_amdgcn_readfirstlane(tile.sub) * BN;
@@ -165,7 +165,7 @@ hipError_t run(const GmmArgs& a, hipStream_t stream) {
                   a.offsets, a.perm, a.ldx, a.ldw, a.w_group, a.ldy, a.n_rows, a.n_groups,
                   a.k, a.n, (a.n + BN - 1) / BN};
     const int64_t slots = a.n_rows / BM + a.n_groups + 2;
-    const int64_t grid = work_grid(slots * p.n_tiles);
+    const int64_t grid = work_grid(slots, p.n_tiles, false);
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     // no more buffers than stages: short sums leave LDS for more workgroups
     const int stages = (a.k + BK - 1) / BK;

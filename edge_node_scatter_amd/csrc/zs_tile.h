@@ -253,18 +253,23 @@ __device__ inline TileOf tile_at(int64_t v, int64_t index, int64_t step, int64_t
 // Up to this many groups a wavefront adds up all groups' tiles, 64 at a time.
 constexpr int kCountedGroups = 512;
 
-// Workgroups for at most `items` work items: find_work gives an XCD an eighth of
-// each of two kinds, both rounded up.
-inline int64_t work_grid(int64_t items) { return items + 16; }
+// Workgroups for at most `tiles` tiles of `subs` work items: find_work gives an
+// XCD an eighth of each of two kinds, both rounded up, or of each tile.
+inline int64_t work_grid(int64_t tiles, int64_t subs, bool spread) {
+    return spread ? 8 * tiles * ((subs + 7) / 8) : tiles * subs + 16;
+}
 
-// Inclusive sum over the wavefront's lanes.
-__device__ inline uint32_t lane_scan(uint32_t n, int lane) {
-#pragma unroll
-    for (int h = 1; h < 64; h <<= 1) {
-        const uint32_t o = __shfl_up(n, h, 64);
-        if (lane >= h) n += o;
-    }
-    return n;
+// Inclusive sum over the wavefront's lanes: within rows of 16 lanes by shifts,
+// then the last lane of the rows before.
+__device__ inline uint32_t lane_scan(uint32_t n) {
+    int v = int(n);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // lane 15 to the next row
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // lane 31 to the upper half
+    return uint32_t(v);
 }
 
 // The work of workgroup `id`: start(v), v = 0 .. count, are the groups' clamped
@@ -274,7 +279,11 @@ __device__ inline uint32_t lane_scan(uint32_t n, int lane) {
 // Workgroups go to the 8 XCDs in turn, so XCD x, which holds the ids x, x + 8,
 // ..., gets an eighth of the full tiles' items and then an eighth of the
 // part-filled tiles', each in one piece: neighbouring items share its L2, no XCD
-// has more to do than another, and what is dispatched last is short.  (Dealing
+// has more to do than another, and what is dispatched last is short.  With
+// `spread` an XCD instead gets an eighth of every tile's items: for work whose
+// part-filled tiles differ in length, so that the XCDs stay even (8191 rows in 16
+// uneven groups, 776 x 1160 gradients in bf16: CUs busy 52 % of the time without).
+// (Dealing
 // out the ids of the second scheme, whose empty ones fall anywhere, left some
 // XCDs a tile more than they have room for at a time: 16384 rows of 8 equal
 // groups, 512 -> 512 in fp32, took 113 us instead of 83.)
@@ -283,8 +292,8 @@ __device__ inline uint32_t lane_scan(uint32_t n, int lane) {
 // next group's: never fewer than its tiles, increasing with v, and a search over
 // the boundaries, 64 probes at a time, finds a slot's group.
 template <typename Start, typename Least>
-__device__ inline TileOf find_work(uint32_t id, uint32_t grid, int subs, int64_t count,
-                                   int64_t step, Start start, Least least) {
+__device__ inline TileOf find_work(uint32_t id, uint32_t grid, int subs, bool spread,
+                                   int64_t count, int64_t step, Start start, Least least) {
     const int lane = threadIdx.x & 63;
     TileOf none{};
     none.group = -1;
@@ -293,54 +302,90 @@ __device__ inline TileOf find_work(uint32_t id, uint32_t grid, int subs, int64_t
     if (count <= kCountedGroups) {
         constexpr int kChunks = kCountedGroups / 64;
         const int chunks = int((count + 63) / 64);
-        // full tiles and part-filled ones of this lane's groups, summed up to it
-        uint32_t before[2][kChunks], total[2] = {0, 0};
+        // of this lane's groups: first position, rows, full tiles up to it, whether
+        // it has a part-filled tile
+        uint32_t at[kChunks], rows[kChunks], before[kChunks];
+        uint64_t part[kChunks];
+        uint32_t total[2] = {0, 0};
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-            before[0][c] = before[1][c] = 0;
+            at[c] = rows[c] = before[c] = 0;
+            part[c] = 0;
             if (c >= chunks) continue;
             const int64_t v = c * 64 + lane;
-            uint32_t full = 0, part = 0;
+            uint32_t full = 0;
+            bool more = false;
             if (v < count) {
                 const int64_t a = start(v), b = start(v + 1);
-                const uint32_t rows = b > a ? uint32_t(b - a) : 0;
-                full = rows / uint32_t(step);
-                part = full * uint32_t(step) < rows || (rows == 0 && least(v) > 0) ? 1 : 0;
+                at[c] = uint32_t(a);
+                rows[c] = b > a ? uint32_t(b - a) : 0;
+                full = rows[c] / uint32_t(step);
+                more = full * uint32_t(step) < rows[c] || (rows[c] == 0 && least(v) > 0);
             }
-            before[0][c] = total[0] + lane_scan(full, lane);
-            before[1][c] = total[1] + lane_scan(part, lane);
-            total[0] = __builtin_amdgcn_readlane(before[0][c], 63);
-            total[1] = __builtin_amdgcn_readlane(before[1][c], 63);
+            before[c] = total[0] + lane_scan(full);
+            part[c] = __ballot(more);
+            total[0] = __builtin_amdgcn_readlane(before[c], 63);
+            total[1] += uint32_t(__popcll(part[c]));
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const uint64_t items = uint64_t(total[k]) * uint32_t(subs);
-            const uint64_t per = items / 8, rest = items % 8;
-            const uint32_t mine = uint32_t(per) + (xcd < rest ? 1 : 0);
-            if (nth >= mine) {
-                nth -= mine;
-                continue;
+            uint32_t tile;
+            int sub;
+            if (spread) {
+                const uint32_t first = uint32_t(subs) * xcd / 8,
+                               mine = uint32_t(subs) * (xcd + 1) / 8 - first;
+                tile = nth / mine;
+                sub = int(first + nth - tile * mine);
+                if (tile >= total[k]) {
+                    nth -= total[k] * mine;
+                    continue;
+                }
+            } else {
+                const uint64_t items = uint64_t(total[k]) * uint32_t(subs);
+                const uint64_t per = items / 8, rest = items % 8;
+                const uint32_t mine = uint32_t(per) + (xcd < rest ? 1 : 0);
+                if (nth >= mine) {
+                    nth -= mine;
+                    continue;
+                }
+                const uint64_t item = xcd * per + (xcd < rest ? xcd : rest) + nth;
+                tile = uint32_t(item / uint32_t(subs));
+                sub = int(item - uint64_t(tile) * uint32_t(subs));
             }
-            const uint64_t item = xcd * per + (xcd < rest ? xcd : rest) + nth;
-            const uint32_t tile = uint32_t(item / uint32_t(subs));
             uint32_t base = 0;
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
                 if (c >= chunks) continue;
-                const uint32_t last = __builtin_amdgcn_readlane(before[k][c], 63);
-                if (tile < last) {
-                    // lanes whose groups lie before the tile's
-                    const int l = __popcll(__ballot(before[k][c] <= tile));
-                    const uint32_t first =
-                        l > 0 ? uint32_t(__shfl(before[k][c], l - 1, 64)) : base;
-                    const int64_t v = c * 64 + l, a = start(v), b = start(v + 1);
-                    const uint32_t index =
-                        k == 0 ? tile - first : (b > a ? uint32_t(b - a) / uint32_t(step) : 0);
-                    TileOf t = tile_at(v, index, step, a, b);
-                    t.sub = int(item - uint64_t(tile) * uint32_t(subs));
+                int l = -1;
+                uint32_t index = 0;
+                if (k == 0) {
+                    if (tile < uint32_t(__builtin_amdgcn_readlane(before[c], 63))) {
+                        // lanes whose groups lie before the tile's
+                        l = __popcll(__ballot(before[c] <= tile));
+                        index = tile - (l > 0 ? uint32_t(__builtin_amdgcn_readlane(before[c], l - 1))
+                                              : base);
+                    }
+                    base = __builtin_amdgcn_readlane(before[c], 63);
+                } else {
+                    const uint32_t here = uint32_t(__popcll(part[c]));
+                    if (tile < here) {
+                        // the lane of the tile-th part-filled tile: it has `tile` before it
+                        const uint32_t mine_before = __builtin_amdgcn_mbcnt_hi(
+                            uint32_t(part[c] >> 32),
+                            __builtin_amdgcn_mbcnt_lo(uint32_t(part[c]), 0));
+                        l = __ffsll(__ballot(mine_before == tile && ((part[c] >> lane) & 1))) - 1;
+                        index = uint32_t(__builtin_amdgcn_readlane(rows[c], l)) / uint32_t(step);
+                    } else {
+                        tile -= here;
+                    }
+                }
+                if (l >= 0) {
+                    const int64_t a = uint32_t(__builtin_amdgcn_readlane(at[c], l));
+                    const int64_t n = uint32_t(__builtin_amdgcn_readlane(rows[c], l));
+                    TileOf t = tile_at(c * 64 + l, index, step, a, a + n);
+                    t.sub = sub;
                     return t;
                 }
-                base = last;
             }
         }
         return none;

@@ -23,6 +23,7 @@ struct WgParams {
     const int32_t* perm;
     int64_t ldx, ldg, n_rows, n_groups, piece;
     int k, n, k_tiles, n_tiles;
+    bool spread;   // each XCD takes an eighth of every piece's tiles
 };
 
 __device__ inline int64_t clamp_offset(const int32_t* offsets, int64_t v, int64_t n_rows) {
@@ -55,8 +56,8 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const auto start = [&](int64_t v) { return clamp_offset(p.offsets, v, p.n_rows); };
-    const TileOf tile = find_work(blockIdx.x, gridDim.x, p.k_tiles * p.n_tiles, p.n_groups,
-                                  p.piece, start, [](int64_t) { return 1; });
+    const TileOf tile = find_work(blockIdx.x, gridDim.x, p.k_tiles * p.n_tiles, p.spread,
+                                  p.n_groups, p.piece, start, [](int64_t) { return 1; });
     if (tile.group < 0) return;
     const int in_slot = __builtin_amdgcn_readfirstlane(tile.sub);
     const int a0 = in_slot / p.n_tiles * BA, n0 = in_slot % p.n_tiles * BN;
@@ -106,7 +107,8 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
             char* to = buf + (wave * IA + i) * 1024;
             const int32_t r = index[at + ar[i]];
             const bool in = r >= 0 && ac[i] < p.k;
-            const T* src = p.x + r * p.ldx + ac[i];
+            // VEC: strides of 32 bits, one multiply-add
+            const T* src = p.x + (VEC ? int64_t(uint64_t(uint32_t(r)) * uint32_t(p.ldx)) : r * p.ldx) + ac[i];
             if constexpr (VEC)
                 load_to_lds(in ? static_cast<const void*>(src) : zero_chunk, lds_offset(to));
             else
@@ -117,7 +119,7 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
             char* to = buf + kABytes + (wave * IB + i) * 1024;
             const int32_t r = index[at + br[i]];
             const bool in = r >= 0 && bc[i] < p.n;
-            const T* src = p.gy + r * p.ldg + bc[i];
+            const T* src = p.gy + (VEC ? int64_t(uint64_t(uint32_t(r)) * uint32_t(p.ldg)) : r * p.ldg) + bc[i];
             if constexpr (VEC)
                 load_to_lds(in ? static_cast<const void*>(src) : zero_chunk, lds_offset(to));
             else
@@ -238,8 +240,10 @@ template <typename T, int BA, int BN, bool VEC>
 hipError_t run(WgParams<T> p, hipStream_t stream) {
     constexpr int S = 2, KB = 128, BR = KB / sizeof(T);
     p.k_tiles = (p.k + BA - 1) / BA, p.n_tiles = (p.n + BN - 1) / BN;
+    // below that an eighth of a tile's items is too coarse a share
+    p.spread = p.k_tiles * p.n_tiles >= 16 && p.n_groups <= kCountedGroups;
     const int64_t slots = p.n_rows / p.piece + p.n_groups;
-    const int64_t grid = work_grid(slots * p.k_tiles * p.n_tiles);
+    const int64_t grid = work_grid(slots, int64_t(p.k_tiles) * p.n_tiles, p.spread);
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     const int64_t longest = p.piece < p.n_rows ? p.piece : p.n_rows;
     const int stages = int((longest + BR - 1) / BR);
@@ -270,9 +274,9 @@ hipError_t dispatch(const WgradArgs& a, hipStream_t stream) {
     const auto on16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     WgParams<T> p{static_cast<const T*>(a.x), static_cast<const T*>(a.gy), static_cast<T*>(a.gw),
                   a.partial, a.offsets, a.perm, a.ldx, a.ldg, a.n_rows, a.n_groups, a.piece,
-                  a.k, a.n, 0, 0};
+                  a.k, a.n, 0, 0, false};
     const bool vec = on16(a.x) && a.ldx % E == 0 && a.k % E == 0 && on16(a.gy) && a.ldg % E == 0 &&
-                     a.n % E == 0;
+                     a.n % E == 0 && a.ldx <= INT32_MAX && a.ldg <= INT32_MAX;
     hipError_t err;
     if (!vec)
         err = run<T, 64, 64, false>(p, stream);
