@@ -54,6 +54,8 @@ def load_block() -> ctypes.CDLL:
             "zs_grouped_mm_wgrad_workspace_bytes": ([I64, I64, I64, I64, INT], SZ),
             "zs_grouped_mm_wgrad": ([P, I64, P, I64, P, P, I64, I64, I64, I64, INT, P, P, SZ, P],
                                     INT),
+            "zs_grouped_mm_backward": ([P, I64, P, I64, P, I64, I64, P, P, I64, I64, I64, I64, INT,
+                                        P, P, P, SZ, P], INT),
             "zs_block_join": ([P, I64, P, I64, P, I64, I64, P, P, P, I64, I64, F32, INT, P, P, P],
                               INT),
             "zs_block_join_workspace_bytes": ([I64, I64], SZ),
@@ -160,6 +162,11 @@ def zs_grouped_mm(x: torch.Tensor, w: torch.Tensor, groups: Csr,
     return out
 
 
+def _wgrad_workspace(M, n_groups, k, n, x):
+    size = load_block().zs_grouped_mm_wgrad_workspace_bytes(M, n_groups, k, n, DTYPES[x.dtype])
+    return torch.empty(size, dtype=torch.uint8, device=x.device) if size else None, size
+
+
 def zs_grouped_mm_backward(grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor, groups: Csr,
                            need_x: bool = True, need_w: bool = True):
     """(grad_x (M, k), grad_w (G, k, n)) of zs_grouped_mm; None for one that is
@@ -173,6 +180,15 @@ def zs_grouped_mm_backward(grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tenso
     grad_y = _rows(grad_y)
     w, transposed = _weights(w)
     gx = gw = None
+    if need_x and need_w and not transposed:
+        gx = torch.empty((M, k), dtype=x.dtype, device=x.device)
+        gw = torch.empty((groups.n_nodes, k, n), dtype=x.dtype, device=x.device)
+        ws, size = _wgrad_workspace(M, groups.n_nodes, k, n, x)
+        _check("zs_grouped_mm_backward", _call(
+            x.device, load_block().zs_grouped_mm_backward, _ptr(grad_y), grad_y.stride(0), _ptr(x),
+            x.stride(0), _ptr(w), w.stride(0), w.stride(1), _ptr(groups.rowptr), _ptr(groups.perm),
+            M, groups.n_nodes, k, n, DTYPES[x.dtype], _ptr(gx), _ptr(gw), _ptr(ws), size))
+        return gx, gw
     if need_x:
         gx = torch.empty((M, k), dtype=x.dtype, device=x.device)
         # the memory [k][n] read as the [n][k] of the transposed product
@@ -181,12 +197,9 @@ def zs_grouped_mm_backward(grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tenso
     if need_w:
         a, b = (grad_y, x) if transposed else (x, grad_y)
         gw = torch.empty((groups.n_nodes, a.shape[1], b.shape[1]), dtype=x.dtype, device=x.device)
-        lib = load_block()
-        size = lib.zs_grouped_mm_wgrad_workspace_bytes(M, groups.n_nodes, a.shape[1], b.shape[1],
-                                                       DTYPES[x.dtype])
-        ws = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
+        ws, size = _wgrad_workspace(M, groups.n_nodes, a.shape[1], b.shape[1], x)
         _check("zs_grouped_mm_wgrad", _call(
-            x.device, lib.zs_grouped_mm_wgrad, _ptr(a), a.stride(0), _ptr(b), b.stride(0),
+            x.device, load_block().zs_grouped_mm_wgrad, _ptr(a), a.stride(0), _ptr(b), b.stride(0),
             _ptr(groups.rowptr), _ptr(groups.perm), M, groups.n_nodes, a.shape[1], b.shape[1],
             DTYPES[x.dtype], _ptr(gw), _ptr(ws), size))
         if transposed:

@@ -119,8 +119,53 @@ int zs_grouped_mm_wgrad(const void* x, int64_t x_stride, const void* grad_y, int
     if (aliased(outs, 2, ins, 4)) return ZS_ERR_ALIAS;
     const zs::WgradArgs a{x,        grad_y,    grad_w, static_cast<float*>(workspace),
                           offsets,  perm,      x_stride, gy_stride,
-                          n_rows,   n_groups,  plan.piece, int(k), int(n)};
+                          n_rows,   n_groups,  plan.piece, int(k), int(n), nullptr, nullptr, 0, 0};
     return hip_status(zs::launch_wgrad(a, dtype == ZS_BF16, static_cast<hipStream_t>(stream)));
+}
+
+int zs_grouped_mm_backward(const void* grad_y, int64_t gy_stride, const void* x, int64_t x_stride,
+                           const void* w, int64_t w_group_stride, int64_t w_stride,
+                           const int32_t* offsets, const int32_t* perm, int64_t n_rows,
+                           int64_t n_groups, int64_t k, int64_t n, int dtype, void* grad_x,
+                           void* grad_w, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!mm_sizes_ok(n_rows, n_groups, k, n)) return ZS_ERR_SHAPE;
+    if (!dtype_ok(dtype)) return ZS_ERR_UNSUPPORTED;
+    if (x_stride < 0 || gy_stride < 0 || w_stride < 0 || w_group_stride < 0) return ZS_ERR_SHAPE;
+    const int64_t ex = extent(n_rows, x_stride, k), eg = extent(n_rows, gy_stride, n),
+                  e1 = extent(k, w_stride, n);
+    const int64_t ew = e1 < 0 ? -1 : extent(n_groups, w_group_stride, e1);
+    if (ex < 0 || eg < 0 || ew < 0) return ZS_ERR_SHAPE;
+    if (!offsets || !grad_w || (n_rows > 0 && (!x || !grad_y || !w || !grad_x))) return ZS_ERR_NULL;
+    const int64_t es = size_of(dtype);
+    if (!aligned(x, es) || !aligned(grad_y, es) || !aligned(w, es) || !aligned(grad_x, es) ||
+        !aligned(grad_w, es) || !aligned(offsets, 4) || !aligned(perm, 4))
+        return ZS_ERR_UNSUPPORTED;
+    const zs::WgradPlan plan = zs::plan_wgrad(n_rows, n_groups, k, n, dtype == ZS_BF16);
+    if (plan.bytes > 0) {
+        if (!workspace || workspace_bytes < plan.bytes) return ZS_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return ZS_ERR_UNSUPPORTED;
+    }
+    const Range outs[] = {span(grad_w, n_groups * k * n * es), span(grad_x, n_rows * k * es),
+                          span(plan.bytes ? workspace : nullptr, int64_t(plan.bytes))};
+    const Range ins[] = {span(x, ex * es), span(grad_y, eg * es), span(w, ew * es),
+                         span(offsets, (n_groups + 1) * 4), span(perm, n_rows * 4)};
+    if (aliased(outs, 3, ins, 5)) return ZS_ERR_ALIAS;
+    const bool bf16 = dtype == ZS_BF16;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    zs::WgradArgs a{x,      grad_y,   grad_w,     static_cast<float*>(workspace),
+                    offsets, perm,    x_stride,   gy_stride,
+                    n_rows, n_groups, plan.piece, int(k), int(n), w, grad_x, w_stride,
+                    w_group_stride};
+    if (n_rows == 0 || !zs::both_gradients(a, bf16)) {
+        a.gx = nullptr;
+        if (n_rows > 0) {
+            const zs::GmmArgs g{grad_y,  w,        grad_x,         offsets, perm,     gy_stride,
+                                w_stride, w_group_stride, k, n_rows,  n_groups, int(n), int(k)};
+            const hipError_t err = zs::launch_gmm(g, bf16, true, s);
+            if (err != hipSuccess) return ZS_ERR_HIP;
+        }
+    }
+    return hip_status(zs::launch_wgrad(a, bf16, s));
 }
 
 }  // extern "C"

@@ -33,7 +33,13 @@ struct WgradArgs {
     int64_t n_rows, n_groups;
     int64_t piece;   // rows of a piece; above n_rows: groups are never cut
     int k, n;
+    // where both_gradients() says so: grad_x [n_rows][k] too, from w [k][n]
+    const void* w;
+    void* gx;
+    int64_t ldw, w_group;
 };
+// Whether one kernel forms both gradients: the weights are one tile.
+bool both_gradients(const WgradArgs& a, bool bf16);
 
 // How the weight gradient is cut: rows per piece and the bytes its partial
 // sums take (0: no group is cut).

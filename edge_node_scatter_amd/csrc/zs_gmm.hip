@@ -135,7 +135,8 @@ __global__ __launch_bounds__(WM * WN * 64) void zs_gmm_kernel(const MmParams<T> 
                     return read_row_frag<T, KB>(at + kABytes, wn * NT + j, s, lane);
                 else
                     return read_sum_frag<T, LN>(at + kABytes, wn * NT + j, s, lane);
-            });
+            },
+            [](int, const char*) {});
     }
 
     const bool wide = p.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(p.y) % (4 * sizeof(T)) == 0;

@@ -11,7 +11,7 @@
 // row (XOR with a function of the row) so that a fragment's reads fall on
 // different banks.
 //
-// mma16 multiplies 16 x 16 output tiles: lane l holds kept index l % 16 of
+// Matrix instructions multiply 16 x 16 output tiles: lane l holds kept index l % 16 of
 // both operands and, in the sub-stage of 64 bytes, the summed indices of its
 // 16-byte share l / 16.  fp32 uses four 16x16x4 steps whose summed indices are
 // 4 (l / 16) + step on both sides, so that a lane's share is contiguous too;
@@ -75,14 +75,18 @@ struct Frag<__bf16> {
     using V = bf16x8;
 };
 
-__device__ inline f32x4 mma16(bf16x8 a, bf16x8 b, f32x4 acc) {
+// One step of a 16 x 16 product: all of a bf16 fragment, a quarter of an fp32 one.
+// The steps of several tiles are taken in turn, so that an instruction does not
+// wait for the one before it.
+template <typename T>
+constexpr int mma_steps() {
+    return sizeof(T) == 4 ? 4 : 1;
+}
+__device__ inline f32x4 mma_step(bf16x8 a, bf16x8 b, f32x4 acc, int) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
 }
-__device__ inline f32x4 mma16(f32x4 a, f32x4 b, f32x4 acc) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], acc, 0, 0, 0);
-    return acc;
+__device__ inline f32x4 mma_step(f32x4 a, f32x4 b, f32x4 acc, int step) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a[step], b[step], acc, 0, 0, 0);
 }
 
 // ---- row form -------------------------------------------------------------
@@ -101,11 +105,13 @@ __device__ inline typename Frag<T>::V read_row_frag(const char* tile, int t, int
 }
 
 // ---- sum form, W kept indices per row ---------------------------------------
+// Spreads both kinds of read over the banks: the transposed reads of the summed
+// index, and reads of 16 rows at one chunk (the row form of the same tile).
 template <typename T, int W>
 __device__ inline int sum_swizzle(int k) {
-    if constexpr (sizeof(T) == 4) return 4 * ((k >> 2) & (W / 16 >= 4 ? 3 : W / 16 - 1));
+    if constexpr (sizeof(T) == 4) return 4 * ((k >> 2) & (W / 16 >= 4 ? 3 : W / 16 - 1)) | (k & 3);
     constexpr int pairs = W / 16;   // 32-byte pairs of chunks in a row
-    return 2 * (((k & 3) | ((k >> 1) & 4)) & (pairs - 1));
+    return 2 * (((k & 3) | ((k >> 1) & 4)) & (pairs - 1)) | ((k >> 2) & 1);
 }
 
 // bf16: two transposed LDS reads; in each, 16 lanes read 4 rows of 16 kept
@@ -138,6 +144,15 @@ __device__ inline f32x4 read_sum_frag_f32(const char* tile, int t, int s, int la
         v[j] = *reinterpret_cast<const float*>(tile + k * (W * 4) + chunk * 16 + (n & 3) * 4);
     }
     return v;
+}
+// Row-form fragment of a sum-form tile: tile rows 16 t .. 16 t + 15 as kept
+// indices, the 64 bytes s of their columns as summed ones.
+template <typename T, int W>
+__device__ inline typename Frag<T>::V read_rows_of_sum(const char* tile, int t, int s, int lane) {
+    const int row = t * 16 + (lane & 15);
+    const int chunk = (s * 4 + (lane >> 4)) ^ sum_swizzle<T, W>(row);
+    return *reinterpret_cast<const typename Frag<T>::V*>(tile + row * (W * int(sizeof(T))) +
+                                                         chunk * 16);
 }
 template <typename T, int W>
 __device__ inline typename Frag<T>::V read_sum_frag(const char* tile, int t, int s, int lane) {
@@ -174,16 +189,17 @@ __device__ inline void store4(T* p, f32x4 v) {
 
 // The product loop over `stages` stages, S buffers of kBytes deep.  issue(i, buf)
 // starts the loads of stage i (kLoads per wavefront); read_a(buf, i, s) and
-// read_b(buf, j, s) read fragments of sub-stage s.  One barrier a stage: it
+// read_b(buf, j, s) read fragments of sub-stage s; also(i, buf) does what else a
+// stage is for.  One barrier a stage: it
 // publishes the stage and says that every wavefront is done with the one before,
 // whose buffer the next loads fill.  (Reading the fragments of the next sub-stage
 // ahead, across the barrier, was no faster in the products and slower in the
 // weight gradient, whose transposed reads then crowd its registers: 16384 x
 // 4096 x 4096 in bf16 495 us either way, its weight gradient 680 and 775.)
 template <typename T, int MT, int NT, int KB, int S, int kBytes, int kLoads, typename Issue,
-          typename ReadA, typename ReadB>
+          typename ReadA, typename ReadB, typename Also>
 __device__ inline void product_loop(int stages, char* lds, f32x4 (&acc)[MT][NT], Issue issue,
-                                    ReadA read_a, ReadB read_b) {
+                                    ReadA read_a, ReadB read_b, Also also) {
     using V = typename Frag<T>::V;
     constexpr int NS = KB / 64;
     if (stages <= 0) return;
@@ -209,10 +225,14 @@ __device__ inline void product_loop(int stages, char* lds, f32x4 (&acc)[MT][NT],
 #pragma unroll
             for (int i = 0; i < MT; ++i) a[i] = read_a(at, i, s);
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+            for (int step = 0; step < mma_steps<T>(); ++step)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) acc[i][j] = mma16(b[j], a[i], acc[i][j]);
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        acc[i][j] = mma_step(b[j], a[i], acc[i][j], step);
         }
+        also(stage, at);
     }
 }
 

@@ -6,6 +6,10 @@
 // `piece` rows) of one group.  A group of one piece is written at once; the
 // pieces of a longer one leave fp32 partial sums that a second kernel adds in
 // order.
+//
+// Narrow weights (one tile, which the wavefronts also hold as fragments): the
+// same pass forms grad_x[i] = grad_y[i] w[g]^T from the rows of grad_y that lie in
+// LDS for the weight gradient, so that they are read once.
 #include "zs_block_internal.h"
 #include "zs_tile.h"
 
@@ -23,6 +27,10 @@ struct WgParams {
     const int32_t* perm;
     int64_t ldx, ldg, n_rows, n_groups, piece;
     int k, n, k_tiles, n_tiles;
+    // both gradients at once
+    const T* w;
+    T* gx;
+    int64_t ldw, w_group;
     bool spread;   // each XCD takes an eighth of every piece's tiles
 };
 
@@ -40,8 +48,8 @@ __device__ inline int64_t first_piece(int64_t start, int64_t piece) { return 2 *
 constexpr int pow2_at_least(int v) { return v <= 32 ? 32 : v <= 64 ? 64 : 128; }
 constexpr int kIndexRows = 1024;   // row indices kept in LDS at a time
 
-// VEC as in the grouped products.
-template <typename T, int BA, int BN, int WA, int WN, int KB, int S, bool VEC>
+// VEC as in the grouped products.  BOTH: grad_x too; k <= BA and n <= BN.
+template <typename T, int BA, int BN, int WA, int WN, int KB, int S, bool VEC, bool BOTH>
 __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T> p) {
     constexpr int kWaves = WA * WN;
     constexpr int E = 16 / sizeof(T);
@@ -55,13 +63,27 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
     __shared__ int32_t index[kIndexRows];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const auto start = [&](int64_t v) { return clamp_offset(p.offsets, v, p.n_rows); };
+    // BOTH: groups -1 and n_groups are the rows of no group, whose grad_x is zero
+    const auto start = [&](int64_t v) -> int64_t {
+        if (BOTH && v == 0) return 0;
+        if (BOTH && v == p.n_groups + 2) return p.n_rows;
+        return clamp_offset(p.offsets, BOTH ? v - 1 : v, p.n_rows);
+    };
+    const auto least = [&](int64_t v) { return BOTH && (v == 0 || v == p.n_groups + 1) ? 0 : 1; };
     const TileOf tile = find_work(blockIdx.x, gridDim.x, p.k_tiles * p.n_tiles, p.spread,
-                                  p.n_groups, p.piece, start, [](int64_t) { return 1; });
+                                  p.n_groups + (BOTH ? 2 : 0), p.piece, start, least);
     if (tile.group < 0) return;
     const int in_slot = __builtin_amdgcn_readfirstlane(tile.sub);
     const int a0 = in_slot / p.n_tiles * BA, n0 = in_slot % p.n_tiles * BN;
-    const int group = __builtin_amdgcn_readfirstlane(tile.group);
+    const int group = __builtin_amdgcn_readfirstlane(tile.group) - (BOTH ? 1 : 0);
+    if (BOTH && (group < 0 || group >= p.n_groups)) {
+        for (int64_t i = threadIdx.x; i < (tile.end - tile.begin) * p.k; i += kWaves * 64) {
+            const int64_t pos = tile.begin + i / p.k;
+            const int64_t r = p.perm ? p.perm[pos] : pos;
+            if (r >= 0 && r < p.n_rows) p.gx[r * p.k + i % p.k] = T(0);
+        }
+        return;
+    }
 
     f32x4 acc[AT][NT];
 #pragma unroll
@@ -126,6 +148,30 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
                 *reinterpret_cast<u32x4*>(to + lane * 16) = load_partial(src, in ? p.n - bc[i] : 0);
         }
     };
+    // BOTH: a wavefront forms grad_x of 16 of a stage's rows, in fp32 (stages of 32
+    // rows) half of their columns; its fragments of w have the columns as the fast
+    // index (in bf16 in pairs of tiles whose columns alternate by four, so that a
+    // lane's results of a pair are eight neighbours) and n as the summed one
+    constexpr int RT = BR / 16, KS = kWaves / RT, XT = BA / 16 / KS, NC = LN * int(sizeof(T)) / 64;
+    static_assert(!BOTH || (RT * KS == kWaves && XT >= 1), "wavefronts do not cover a stage");
+    const int rt = wave % RT, x0 = wave / RT * XT;
+    const auto column = [&](int t, int i) {
+        if (sizeof(T) == 4) return (x0 + t) * 16 + i;
+        return (t >> 1) * 32 + (i >> 2) * 8 + (t & 1) * 4 + (i & 3);
+    };
+    typename Frag<T>::V w[BOTH ? XT : 1][BOTH ? NC : 1];
+    int32_t out_row[2] = {-1, -1};   // this lane's row of even and odd stages
+    if constexpr (BOTH) {
+#pragma unroll
+        for (int t = 0; t < XT; ++t)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int k = column(t, lane & 15), n = (c * 4 + (lane >> 4)) * E;
+                const T* from = p.w + group * p.w_group + k * p.ldw + n;
+                w[t][c] = __builtin_bit_cast(typename Frag<T>::V,
+                                             load_partial(from, k < p.k ? p.n - n : 0));
+            }
+    }
     // a stage's loads, with the row indices they need in LDS
     const auto issue = [&](int stage, char* buf) {
         if (stage * BR % kIndexRows == 0) {
@@ -133,18 +179,59 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
             fill(stage * BR);
             tile_barrier();
         }
+        if constexpr (BOTH) {
+            const int32_t r = index[stage * BR % kIndexRows + rt * 16 + (lane & 15)];
+            out_row[0] = stage & 1 ? out_row[0] : r;
+            out_row[1] = stage & 1 ? r : out_row[1];
+        }
         load(stage, buf);
+    };
+    const auto rows_of_x = [&](int stage, const char* at) {
+        if constexpr (BOTH) {
+            f32x4 x[XT];
+#pragma unroll
+            for (int t = 0; t < XT; ++t) x[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const auto g = read_rows_of_sum<T, LN>(at + kABytes, rt, c, lane);
+#pragma unroll
+                for (int step = 0; step < mma_steps<T>(); ++step)
+#pragma unroll
+                    for (int t = 0; t < XT; ++t) x[t] = mma_step(w[t][c], g, x[t], step);
+            }
+            const int64_t r = stage & 1 ? out_row[1] : out_row[0];
+            if (r < 0) return;
+            T* to = p.gx + r * p.k;
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int t = 0; t < XT; ++t) {
+                    const int k = (x0 + t) * 16 + 4 * (lane >> 4);
+                    if (k < p.k) store4(to + k, x[t]);
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < XT; t += 2) {
+                    const int k = t * 16 + 8 * (lane >> 4);
+                    const bf16x4 lo = __builtin_convertvector(x[t], bf16x4),
+                                 hi = __builtin_convertvector(x[t + 1], bf16x4);
+                    if (k < p.k)
+                        *reinterpret_cast<bf16x8*>(to + k) =
+                            __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                }
+            }
+        }
     };
     product_loop<T, AT, NT, KB, S, kBytes, IA + IB>(
         stages, lds, acc, issue,
         [&](const char* at, int i, int s) { return read_sum_frag<T, BA>(at, wa * AT + i, s, lane); },
         [&](const char* at, int j, int s) {
             return read_sum_frag<T, LN>(at + kABytes, wn * NT + j, s, lane);
-        });
+        },
+        rows_of_x);
 
     const bool whole = tile.tiles <= 1;   // the group's only piece
     const bool wide = p.n % 4 == 0 && reinterpret_cast<uintptr_t>(p.gw) % 16 == 0;
-    const int64_t slot = first_piece(start(group), p.piece) + tile.index;
+    const int64_t slot = first_piece(clamp_offset(p.offsets, group, p.n_rows), p.piece) + tile.index;
     float* part = p.partial + slot * int64_t(p.k) * p.n;
     T* out = p.gw + group * int64_t(p.k) * p.n;
 #pragma unroll
@@ -236,19 +323,19 @@ __global__ __launch_bounds__(256) void zs_wgrad_sum_kernel(const WgParams<T> p) 
     }
 }
 
-template <typename T, int BA, int BN, bool VEC>
+template <typename T, int BA, int BN, bool VEC, bool BOTH = false>
 hipError_t run(WgParams<T> p, hipStream_t stream) {
     constexpr int S = 2, KB = 128, BR = KB / sizeof(T);
     p.k_tiles = (p.k + BA - 1) / BA, p.n_tiles = (p.n + BN - 1) / BN;
     // below that an eighth of a tile's items is too coarse a share
     p.spread = p.k_tiles * p.n_tiles >= 16 && p.n_groups <= kCountedGroups;
-    const int64_t slots = p.n_rows / p.piece + p.n_groups;
+    const int64_t slots = p.n_rows / p.piece + p.n_groups + (BOTH ? 2 : 0);
     const int64_t grid = work_grid(slots, int64_t(p.k_tiles) * p.n_tiles, p.spread);
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     const int64_t longest = p.piece < p.n_rows ? p.piece : p.n_rows;
     const int stages = int((longest + BR - 1) / BR);
     const int bytes = (stages < 1 ? 1 : stages < S ? stages : S) * (BA + pow2_at_least(BN)) * KB;
-    auto* kernel = zs_wgrad_kernel<T, BA, BN, 2, 2, KB, S, VEC>;
+    auto* kernel = zs_wgrad_kernel<T, BA, BN, 2, 2, KB, S, VEC, BOTH>;
     if (bytes + 4 * kIndexRows > 65536) {
         const hipError_t err = hipFuncSetAttribute(
             reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -258,34 +345,43 @@ hipError_t run(WgParams<T> p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <typename T, int BA>
+template <typename T, int BA, bool BOTH>
 hipError_t by_n(const WgParams<T>& p, hipStream_t stream) {
     switch (tile_side(p.n, true)) {
-        case 128: return run<T, BA, 128, true>(p, stream);
-        case 96: return run<T, BA, 96, true>(p, stream);
-        case 64: return run<T, BA, 64, true>(p, stream);
-        default: return run<T, BA, 32, true>(p, stream);
+        case 128: return run<T, BA, 128, true, BOTH>(p, stream);
+        case 96: return run<T, BA, 96, true, BOTH>(p, stream);
+        case 64: return run<T, BA, 64, true, BOTH>(p, stream);
+        default: return run<T, BA, 32, true, BOTH>(p, stream);
     }
+}
+
+// Whether the operands' 16-byte chunks start on 16 bytes, strides fit 32 bits.
+bool vectors(const WgradArgs& a, bool bf16) {
+    const int e = bf16 ? 8 : 4;
+    const auto on16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+    return on16(a.x) && a.ldx % e == 0 && a.k % e == 0 && on16(a.gy) && a.ldg % e == 0 &&
+           a.n % e == 0 && a.ldx <= INT32_MAX && a.ldg <= INT32_MAX;
 }
 
 template <typename T>
 hipError_t dispatch(const WgradArgs& a, hipStream_t stream) {
-    constexpr int E = 16 / sizeof(T);
-    const auto on16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     WgParams<T> p{static_cast<const T*>(a.x), static_cast<const T*>(a.gy), static_cast<T*>(a.gw),
                   a.partial, a.offsets, a.perm, a.ldx, a.ldg, a.n_rows, a.n_groups, a.piece,
-                  a.k, a.n, 0, 0, false};
-    const bool vec = on16(a.x) && a.ldx % E == 0 && a.k % E == 0 && on16(a.gy) && a.ldg % E == 0 &&
-                     a.n % E == 0 && a.ldx <= INT32_MAX && a.ldg <= INT32_MAX;
+                  a.k, a.n, 0, 0, static_cast<const T*>(a.w), static_cast<T*>(a.gx), a.ldw,
+                  a.w_group, false};
+    const bool vec = vectors(a, sizeof(T) == 2);
     hipError_t err;
+    const int side = tile_side(a.k, false);
     if (!vec)
         err = run<T, 64, 64, false>(p, stream);
-    else if (tile_side(a.k, false) == 128)
-        err = by_n<T, 128>(p, stream);
-    else if (tile_side(a.k, false) == 64)
-        err = by_n<T, 64>(p, stream);
+    else if (a.gx)
+        err = side == 64 ? by_n<T, 64, true>(p, stream) : by_n<T, 32, true>(p, stream);
+    else if (side == 128)
+        err = by_n<T, 128, false>(p, stream);
+    else if (side == 64)
+        err = by_n<T, 64, false>(p, stream);
     else
-        err = by_n<T, 32>(p, stream);
+        err = by_n<T, 32, false>(p, stream);
     if (err != hipSuccess || a.piece > a.n_rows) return err;
     const int64_t kn = int64_t(a.k) * a.n;
     for (int64_t g0 = 0; g0 < a.n_groups; g0 += 65535) {   // grid.y limit
@@ -317,6 +413,11 @@ WgradPlan plan_wgrad(int64_t n_rows, int64_t n_groups, int64_t k, int64_t n, boo
     if (piece < 256) piece = 256;
     if (piece >= n_rows) return WgradPlan{n_rows + 1, 0};
     return WgradPlan{piece, size_t((2 * n_rows / piece + 1) * k * n * 4)};
+}
+
+bool both_gradients(const WgradArgs& a, bool bf16) {
+    return a.k <= 64 && a.n <= 128 && vectors(a, bf16) &&
+           reinterpret_cast<uintptr_t>(a.gx) % 16 == 0;
 }
 
 hipError_t launch_wgrad(const WgradArgs& a, bool bf16, hipStream_t stream) {

@@ -87,6 +87,22 @@ int zs_grouped_mm_wgrad(const void *x, int64_t x_stride, const void *grad_y,
                         void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * zs_grouped_mm_backward -- both gradients of zs_grouped_mm (weights stored
+ * [k][n]) in one call: grad_x [n_rows][k] and grad_w [n_groups][k][n], both
+ * contiguous, as the two calls above give them up to the order of fp32 sums.
+ * Narrow weights (k <= 64, n <= 128, operands on 16 bytes) take one pass that
+ * reads grad_y once.  Workspace as zs_grouped_mm_wgrad.
+ */
+int zs_grouped_mm_backward(const void *grad_y, int64_t gy_stride, const void *x,
+                           int64_t x_stride, const void *w,
+                           int64_t w_group_stride, int64_t w_stride,
+                           const int32_t *offsets, const int32_t *perm,
+                           int64_t n_rows, int64_t n_groups, int64_t k,
+                           int64_t n, int dtype, void *grad_x, void *grad_w,
+                           void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/*
  * zs_block_join -- the join of a block's output z with its residual stream x,
  * from the norm behind the block to the norm before the next one:
  *

@@ -24,7 +24,7 @@ def lib():
 def test_header_symbols_exported(lib):
     text = open(block.BLOCK_HEADER_PATH).read()
     declared = set(re.findall(r"^\w[\w\s\*]*?\b(zs_\w+)\s*\(", text, flags=re.M))
-    assert declared == {"zs_grouped_mm", "zs_grouped_mm_wgrad_workspace_bytes", "zs_grouped_mm_wgrad", "zs_block_join",
+    assert declared == {"zs_grouped_mm", "zs_grouped_mm_wgrad_workspace_bytes", "zs_grouped_mm_wgrad", "zs_grouped_mm_backward", "zs_block_join",
                         "zs_block_join_workspace_bytes", "zs_block_join_backward", "zs_adamw_step", "zs_adamw_step8",
                         "zs_adamw_moments8"}
     out = subprocess.check_output(["nm", "-D", "--defined-only", zs.LIB_PATH], text=True)
@@ -83,6 +83,24 @@ def test_wgrad_rejects(lib):
     for kw in (dict(ws=None), dict(nb=need - 1), dict(nb=0)):
         assert f(**kw) == WORKSPACE, kw
     for kw in (dict(gw=A), dict(gw=F + 16), dict(ws=B + 256), dict(ws=D)):
+        assert f(**kw) == ALIAS, kw
+
+
+def test_both_gradients_reject(lib):
+    need = lib.zs_grouped_mm_wgrad_workspace_bytes(100000, 3, 8, 8, 0)
+    base = dict(gy=A, ldg=8, x=B, ldx=8, w=C, wg=64, ldw=8, off=D, perm=E, M=100000, G=3, k=8, n=8, dt=0, gx=F, gw=G, ws=H, nb=need, s=None)
+
+    def f(**kw):
+        return lib.zs_grouped_mm_backward(*{**base, **kw}.values())
+    for kw in (dict(M=-1), dict(G=0), dict(k=0), dict(n=65537), dict(ldx=-1), dict(ldg=-1), dict(ldw=-1), dict(wg=-1), dict(wg=1 << 60)):
+        assert f(**kw) == SHAPE, kw
+    for kw in (dict(x=None), dict(gy=None), dict(w=None), dict(off=None), dict(gx=None), dict(gw=None)):
+        assert f(**kw) == NULL, kw
+    for kw in (dict(dt=3), dict(x=B + 2), dict(w=C + 1), dict(gx=F + 2), dict(ws=H + 8)):
+        assert f(**kw) == UNSUPPORTED, kw
+    for kw in (dict(ws=None), dict(nb=need - 1)):
+        assert f(**kw) == WORKSPACE, kw
+    for kw in (dict(gw=C), dict(gx=B), dict(gx=A + 32), dict(gw=F + 64), dict(ws=G), dict(gx=E)):
         assert f(**kw) == ALIAS, kw
 
 
