@@ -125,7 +125,7 @@ __global__ __launch_bounds__(WM * WN * 64) void zs_gmm_kernel(const MmParams<T> 
                     *reinterpret_cast<u32x4*>(to + lane * 16) = load_partial(src, in ? left : 0);
             }
         };
-        product_loop<T, MT, NT, KB, S, kBytes, IA + IB>(
+        product_loop<T, MT, NT, KB, S, kBytes, IA + IB, false>(
             (p.k + BK - 1) / BK, lds, acc, [&](int i, char* buf) { load(i * BK, buf); },
             [&](const char* at, int i, int s) {
                 return read_row_frag<T, KB>(at, wm * MT + i, s, lane);

@@ -552,7 +552,9 @@ template <typename T, int L, int NV>
 hipError_t run(const JoinArgs& a, bool backward, hipStream_t stream) {
     const JoinParams<T> p = params<T>(a);
     const bool all = p.vec && p.z && p.w_pre && (!backward || (p.gy && p.gh));
-    if (all && p.gate_kind == 2) return run_mode<T, L, NV, kFull>(p, backward, stream);
+    // (the widest fp32 rows leave no registers for the sigmoids of a gate per channel)
+    if constexpr (sizeof(T) == 2 || L <= 256)
+        if (all && p.gate_kind == 2) return run_mode<T, L, NV, kFull>(p, backward, stream);
     if (all && p.gate_kind == 1) return run_mode<T, L, NV, kRow>(p, backward, stream);
     return run_mode<T, L, NV, kAny>(p, backward, stream);
 }

@@ -196,8 +196,12 @@ __device__ inline void store4(T* p, f32x4 v) {
 // ahead, across the barrier, was no faster in the products and slower in the
 // weight gradient, whose transposed reads then crowd its registers: 16384 x
 // 4096 x 4096 in bf16 495 us either way, its weight gradient 680 and 775.)
-template <typename T, int MT, int NT, int KB, int S, int kBytes, int kLoads, typename Issue,
-          typename ReadA, typename ReadB, typename Also>
+//
+// LATE (S = 2): also() stores, and stores count as loads do; so it is also()
+// that waits for the next stage's loads, before it stores, and the stores have
+// until the next stage's end.
+template <typename T, int MT, int NT, int KB, int S, int kBytes, int kLoads, bool LATE,
+          typename Issue, typename ReadA, typename ReadB, typename Also>
 __device__ inline void product_loop(int stages, char* lds, f32x4 (&acc)[MT][NT], Issue issue,
                                     ReadA read_a, ReadB read_b, Also also) {
     using V = typename Frag<T>::V;
@@ -209,10 +213,13 @@ __device__ inline void product_loop(int stages, char* lds, f32x4 (&acc)[MT][NT],
     int cur = 0;
     for (int stage = 0; stage < stages; ++stage) {
         // `stage` has arrived when at most the S - 2 stages behind it are in flight
-        if (stage + S - 1 <= stages)
-            wait_loads<(S - 2) * kLoads>();
-        else
-            wait_loads<0>();
+        static_assert(!LATE || S == 2, "also() waits for one stage");
+        if (!LATE || stage == 0) {
+            if (stage + S - 1 <= stages)
+                wait_loads<(S - 2) * kLoads>();
+            else
+                wait_loads<0>();
+        }
         tile_barrier();
         const char* at = lds + cur * kBytes;
         if (stage + S - 1 < stages) issue(stage + S - 1, lds + (cur == 0 ? S - 1 : cur - 1) * kBytes);

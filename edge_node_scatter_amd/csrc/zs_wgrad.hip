@@ -152,7 +152,7 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
     // rows) half of their columns; its fragments of w have the columns as the fast
     // index (in bf16 in pairs of tiles whose columns alternate by four, so that a
     // lane's results of a pair are eight neighbours) and n as the summed one
-    constexpr int RT = BR / 16, KS = kWaves / RT, XT = BA / 16 / KS, NC = LN * int(sizeof(T)) / 64;
+    constexpr int RT = BR / 16, KS = kWaves / RT, XT = BA / 16 / KS, NC = BN * int(sizeof(T)) / 64;
     static_assert(!BOTH || (RT * KS == kWaves && XT >= 1), "wavefronts do not cover a stage");
     const int rt = wave % RT, x0 = wave / RT * XT;
     const auto column = [&](int t, int i) {
@@ -160,7 +160,7 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
         return (t >> 1) * 32 + (i >> 2) * 8 + (t & 1) * 4 + (i & 3);
     };
     typename Frag<T>::V w[BOTH ? XT : 1][BOTH ? NC : 1];
-    int32_t out_row[2] = {-1, -1};   // this lane's row of even and odd stages
+    int32_t even_row = -1, odd_row = -1;   // this lane's row of even and odd stages
     if constexpr (BOTH) {
 #pragma unroll
         for (int t = 0; t < XT; ++t)
@@ -181,8 +181,8 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
         }
         if constexpr (BOTH) {
             const int32_t r = index[stage * BR % kIndexRows + rt * 16 + (lane & 15)];
-            out_row[0] = stage & 1 ? out_row[0] : r;
-            out_row[1] = stage & 1 ? r : out_row[1];
+            even_row = stage & 1 ? even_row : r;
+            odd_row = stage & 1 ? r : odd_row;
         }
         load(stage, buf);
     };
@@ -199,7 +199,8 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
 #pragma unroll
                     for (int t = 0; t < XT; ++t) x[t] = mma_step(w[t][c], g, x[t], step);
             }
-            const int64_t r = stage & 1 ? out_row[1] : out_row[0];
+            wait_loads<0>();   // the next stage's, before the stores
+            const int64_t r = stage & 1 ? odd_row : even_row;
             if (r < 0) return;
             T* to = p.gx + r * p.k;
             if constexpr (sizeof(T) == 4) {
@@ -221,7 +222,7 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
             }
         }
     };
-    product_loop<T, AT, NT, KB, S, kBytes, IA + IB>(
+    product_loop<T, AT, NT, KB, S, kBytes, IA + IB, BOTH>(
         stages, lds, acc, issue,
         [&](const char* at, int i, int s) { return read_sum_frag<T, BA>(at, wa * AT + i, s, lane); },
         [&](const char* at, int j, int s) {
