@@ -101,28 +101,39 @@ __global__ __launch_bounds__(WM * WN * 64) void zs_gmm_kernel(const MmParams<T> 
                 b_ptr[i] = c < BN && b_n[i] < p.n ? w + int64_t(b_k[i]) * p.ldw + b_n[i] : nullptr;
             }
         }
+        // VEC: straight to LDS; otherwise through registers, all loads first
         const auto load = [&](int k0, char* buf) {
+            u32x4 held[VEC ? 1 : IA + IB];
 #pragma unroll
             for (int i = 0; i < IA; ++i) {
-                char* to = buf + (wave * IA + i) * 1024;
                 const int left = p.k - k0 - a_k[i];
                 const bool in = a_ptr[i] && left > 0;
                 const T* src = a_ptr[i] + k0;
                 if constexpr (VEC)
-                    load_to_lds(in ? static_cast<const void*>(src) : zero_chunk, lds_offset(to));
+                    load_to_lds(in ? static_cast<const void*>(src) : zero_chunk,
+                                lds_offset(buf + (wave * IA + i) * 1024));
                 else
-                    *reinterpret_cast<u32x4*>(to + lane * 16) = load_partial(src, in ? left : 0);
+                    held[i] = load_partial(src, in ? left : 0);
             }
 #pragma unroll
             for (int i = 0; i < IB; ++i) {
-                char* to = buf + kABytes + (wave * IB + i) * 1024;
                 const bool in = b_ptr[i] && k0 + b_k[i] < p.k;
                 const T* src = b_ptr[i] + (WT ? int64_t(k0) : int64_t(k0) * p.ldw);
                 const int left = WT ? p.k - k0 - b_k[i] : p.n - b_n[i];
                 if constexpr (VEC)
-                    load_to_lds(in ? static_cast<const void*>(src) : zero_chunk, lds_offset(to));
+                    load_to_lds(in ? static_cast<const void*>(src) : zero_chunk,
+                                lds_offset(buf + kABytes + (wave * IB + i) * 1024));
                 else
-                    *reinterpret_cast<u32x4*>(to + lane * 16) = load_partial(src, in ? left : 0);
+                    held[IA + i] = load_partial(src, in ? left : 0);
+            }
+            if constexpr (!VEC) {
+#pragma unroll
+                for (int i = 0; i < IA; ++i)
+                    *reinterpret_cast<u32x4*>(buf + (wave * IA + i) * 1024 + lane * 16) = held[i];
+#pragma unroll
+                for (int i = 0; i < IB; ++i)
+                    *reinterpret_cast<u32x4*>(buf + kABytes + (wave * IB + i) * 1024 + lane * 16) =
+                        held[IA + i];
             }
         };
         product_loop<T, MT, NT, KB, S, kBytes, IA + IB, false>(
@@ -148,13 +159,10 @@ __global__ __launch_bounds__(WM * WN * 64) void zs_gmm_kernel(const MmParams<T> 
         for (int j = 0; j < NT; ++j) {
             const int n = n0 + (wn * NT + j) * 16 + 4 * (lane >> 4);
             T* to = p.y + r * p.ldy + n;
-            if (wide && n + 4 <= p.n) {
+            if (wide && n + 4 <= p.n)
                 store4(to, acc[i][j]);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (n + q < p.n) to[q] = T(acc[i][j][q]);
-            }
+            else
+                store_partial4(to, acc[i][j], p.n - n);
         }
     }
 }
@@ -187,11 +195,14 @@ hipError_t dispatch(const GmmArgs& a, hipStream_t stream) {
     const auto on16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     const bool vec = on16(a.x) && a.ldx % E == 0 && a.k % E == 0 && on16(a.w) && a.ldw % E == 0 &&
                      a.w_group % E == 0 && (WT || a.n % E == 0);
-    if (!vec) return run<T, 64, 64, 2, 2, 128, 2, WT, false>(a, stream);
     const auto tiles = [&](int bm, int bn) {
         return (a.n_rows / bm + a.n_groups) * ((a.n + bn - 1) / bn);
     };
-    if (tiles(128, 128) < 256) return run<T, 32, 64, 2, 2, 128, 4, WT, true>(a, stream);
+    const bool few = tiles(128, 128) < 256;
+    if (!vec && !few && a.n > 64) return run<T, 128, 128, 2, 2, 128, 2, WT, false>(a, stream);
+    if (!vec) return run<T, 64, 64, 2, 2, 128, 2, WT, false>(a, stream);
+    // tiles too few for the compute units: smaller ones, more stages in flight
+    if (few) return run<T, 32, 64, 2, 2, 128, 4, WT, true>(a, stream);
     const int bn = tile_side(a.n, true);
     if (bn == 128) {
         if constexpr (sizeof(T) == 2)

@@ -162,8 +162,8 @@ __device__ inline typename Frag<T>::V read_sum_frag(const char* tile, int t, int
         return read_sum_frag_f32<W>(tile, t, s, lane);
 }
 
-// Up to 16 bytes of elements, `count` of them valid (others zero), loaded one
-// by one: operands whose rows do not start on 16 bytes.
+// 16 bytes of elements whose first `count` exist (the others zero), from any
+// element's address: one unaligned access where all exist.
 template <typename T>
 __device__ inline u32x4 load_partial(const T* p, int count) {
     constexpr int E = 16 / sizeof(T);
@@ -172,10 +172,26 @@ __device__ inline u32x4 load_partial(const T* p, int count) {
         u32x4 v;
     } u;
     u.v = u32x4{0, 0, 0, 0};
+    if (count >= E) {
+        __builtin_memcpy(&u.v, p, 16);
+    } else {
 #pragma unroll
-    for (int j = 0; j < E; ++j)
-        if (j < count) u.e[j] = p[j];
+        for (int j = 0; j < E; ++j)
+            if (j < count) u.e[j] = p[j];
+    }
     return u.v;
+}
+// Four results to any element's address, the first `count` of them.
+template <typename T>
+__device__ inline void store_partial4(T* p, f32x4 v, int count) {
+    const T e[4] = {T(v[0]), T(v[1]), T(v[2]), T(v[3])};
+    if (count >= 4) {
+        __builtin_memcpy(p, e, 4 * sizeof(T));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < count) p[j] = e[j];
+    }
 }
 
 template <typename T>

@@ -124,28 +124,41 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
     };
     const auto load = [&](int stage, char* buf) {
         const int at = stage * BR % kIndexRows;
+        // VEC: straight to LDS, row offsets of 32-bit strides; otherwise through
+        // registers, all loads first
+        u32x4 held[VEC ? 1 : IA + IB];
 #pragma unroll
         for (int i = 0; i < IA; ++i) {
-            char* to = buf + (wave * IA + i) * 1024;
             const int32_t r = index[at + ar[i]];
             const bool in = r >= 0 && ac[i] < p.k;
-            // VEC: strides of 32 bits, one multiply-add
-            const T* src = p.x + (VEC ? int64_t(uint64_t(uint32_t(r)) * uint32_t(p.ldx)) : r * p.ldx) + ac[i];
-            if constexpr (VEC)
-                load_to_lds(in ? static_cast<const void*>(src) : zero_chunk, lds_offset(to));
-            else
-                *reinterpret_cast<u32x4*>(to + lane * 16) = load_partial(src, in ? p.k - ac[i] : 0);
+            if constexpr (VEC) {
+                const T* src = p.x + uint64_t(uint32_t(r)) * uint32_t(p.ldx) + ac[i];
+                load_to_lds(in ? static_cast<const void*>(src) : zero_chunk,
+                            lds_offset(buf + (wave * IA + i) * 1024));
+            } else {
+                held[i] = load_partial(p.x + r * p.ldx + ac[i], in ? p.k - ac[i] : 0);
+            }
         }
 #pragma unroll
         for (int i = 0; i < IB; ++i) {
-            char* to = buf + kABytes + (wave * IB + i) * 1024;
             const int32_t r = index[at + br[i]];
             const bool in = r >= 0 && bc[i] < p.n;
-            const T* src = p.gy + (VEC ? int64_t(uint64_t(uint32_t(r)) * uint32_t(p.ldg)) : r * p.ldg) + bc[i];
-            if constexpr (VEC)
-                load_to_lds(in ? static_cast<const void*>(src) : zero_chunk, lds_offset(to));
-            else
-                *reinterpret_cast<u32x4*>(to + lane * 16) = load_partial(src, in ? p.n - bc[i] : 0);
+            if constexpr (VEC) {
+                const T* src = p.gy + uint64_t(uint32_t(r)) * uint32_t(p.ldg) + bc[i];
+                load_to_lds(in ? static_cast<const void*>(src) : zero_chunk,
+                            lds_offset(buf + kABytes + (wave * IB + i) * 1024));
+            } else {
+                held[IA + i] = load_partial(p.gy + r * p.ldg + bc[i], in ? p.n - bc[i] : 0);
+            }
+        }
+        if constexpr (!VEC) {
+#pragma unroll
+            for (int i = 0; i < IA; ++i)
+                *reinterpret_cast<u32x4*>(buf + (wave * IA + i) * 1024 + lane * 16) = held[i];
+#pragma unroll
+            for (int i = 0; i < IB; ++i)
+                *reinterpret_cast<u32x4*>(buf + kABytes + (wave * IB + i) * 1024 + lane * 16) =
+                    held[IA + i];
         }
     };
     // BOTH: a wavefront forms grad_x of 16 of a stage's rows, in fp32 (stages of 32
@@ -248,15 +261,10 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
                     store4(out + at, acc[i][j]);
                 else
                     store4(part + at, acc[i][j]);
-                continue;
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (n + q >= p.n) continue;
-                if (whole)
-                    out[at + q] = T(acc[i][j][q]);
-                else
-                    part[at + q] = acc[i][j][q];
+            } else if (whole) {
+                store_partial4(out + at, acc[i][j], p.n - n);
+            } else {
+                store_partial4(part + at, acc[i][j], p.n - n);
             }
         }
     }
@@ -373,7 +381,9 @@ hipError_t dispatch(const WgradArgs& a, hipStream_t stream) {
     const bool vec = vectors(a, sizeof(T) == 2);
     hipError_t err;
     const int side = tile_side(a.k, false);
-    if (!vec)
+    if (!vec && a.k > 64 && a.n > 64)
+        err = run<T, 128, 128, false>(p, stream);
+    else if (!vec)
         err = run<T, 64, 64, false>(p, stream);
     else if (a.gx)
         err = side == 64 ? by_n<T, 64, true>(p, stream) : by_n<T, 32, true>(p, stream);
