@@ -119,9 +119,10 @@ def _check_groups(groups: Csr, n_rows: int, device: torch.device) -> None:
 def _weights(w: torch.Tensor) -> tuple[torch.Tensor, int]:
     """w (G, k, n) and whether its memory is [n][k] (a transposed view, as of
     weights kept output-major); other layouts are copied."""
-    if (w.stride(2) == 1 or w.shape[2] == 1) and w.stride(0) >= 0 and w.stride(1) >= 0:
+    group, row, col = w.stride()
+    if (col == 1 or w.shape[2] == 1) and group >= 0 and row >= 0:
         return w, 0
-    if (w.stride(1) == 1 or w.shape[1] == 1) and w.stride(0) >= 0 and w.stride(2) >= 0:
+    if (row == 1 or w.shape[1] == 1) and group >= 0 and col >= 0:
         return w, 1
     return w.contiguous(), 0
 
@@ -135,11 +136,21 @@ def _mm(x, w, transposed, groups, k, n, out):
 
 
 def _mm_inputs(x, w, groups):
-    x = _typed(x, "x")
-    w = _typed(w, "w", x.dtype, x.device)
-    if x.dim() != 2 or w.dim() != 3 or w.shape[0] != groups.n_nodes or w.shape[1] != x.shape[1]:
-        raise ValueError("x must be (M, k) and w (G, k, n), G the number of groups")
-    _check_groups(groups, x.shape[0], x.device)
+    """x and w, checked against each other and the groups; x with contiguous rows."""
+    dtype, dev, xs, ws = x.dtype, x.device, x.shape, w.shape
+    offsets, perm = groups.rowptr, groups.perm
+    if not (x.is_cuda and dtype in DTYPES and w.dtype == dtype and w.device == dev
+            and len(xs) == 2 and len(ws) == 3 and ws[0] == groups.n_nodes and ws[1] == xs[1]
+            and offsets.dtype == torch.int32 and offsets.device == dev
+            and offsets.shape == (ws[0] + 1,) and offsets.is_contiguous()
+            and (perm is None or perm.dtype == torch.int32 and perm.device == dev
+                 and perm.shape == xs[:1] and perm.is_contiguous())):
+        _typed(x, "x")
+        _typed(w, "w", dtype, dev)
+        if len(xs) != 2 or len(ws) != 3 or ws[0] != groups.n_nodes or ws[1] != xs[1]:
+            raise ValueError("x must be (M, k) and w (G, k, n), G the number of groups")
+        _check_groups(groups, xs[0], dev)
+        raise ValueError("inputs do not fit a grouped product")
     return _rows(x), w
 
 
@@ -152,7 +163,7 @@ def zs_grouped_mm(x: torch.Tensor, w: torch.Tensor, groups: Csr,
     x, w = _mm_inputs(x, w, groups)
     M, n = x.shape[0], w.shape[2]
     if out is None:
-        out = torch.empty((M, n), dtype=x.dtype, device=x.device)
+        out = x.new_empty((M, n))
     else:
         _typed(out, "out", x.dtype, x.device)
         if tuple(out.shape) != (M, n) or (n > 1 and out.stride(1) != 1):
@@ -301,8 +312,8 @@ def zs_block_join(x: torch.Tensor, z: torch.Tensor | None, gate: torch.Tensor | 
     (M, c), (M, 1) or None; scale, w_post and w_pre are float32 (c,).  h is None
     when w_pre is; without z, y is x itself and h its norm."""
     x, z, gate, scale, w_post, w_pre = _join_inputs(x, z, gate, scale, w_post, w_pre)
-    y = x if z is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    h = None if w_pre is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = x if z is None else x.new_empty(x.shape)
+    h = None if w_pre is None else x.new_empty(x.shape)
     _check("zs_block_join", _call(
         x.device, load_block().zs_block_join, *_join_args(x, z, gate, scale, w_post, w_pre, eps),
         None if z is None else _ptr(y), _ptr(h)))
