@@ -3,6 +3,8 @@
 // One workgroup forms a BM x BN tile of one group's rows: x rows (gathered
 // through perm) and the group's weights go through LDS in stages of KB
 // bytes of k, S buffers deep, and the matrix cores accumulate in fp32.
+#include <math.h>
+
 #include "zs_block_internal.h"
 #include "zs_tile.h"
 
@@ -205,8 +207,25 @@ hipError_t dispatch(const GmmArgs& a, hipStream_t stream) {
     if (few) return run<T, 32, 64, 2, 2, 128, 4, WT, true>(a, stream);
     const int bn = tile_side(a.n, true);
     if (bn == 128) {
-        if constexpr (sizeof(T) == 2)
-            if (tiles(256, 256) >= 256) return run<T, 256, 256, 2, 4, 128, 2, WT, true>(a, stream);
+        // bf16 with work for all compute units: tiles of 256 columns, one workgroup a
+        // compute unit; of 256 rows, or of 192 where their last round of workgroups
+        // leaves less idle (a group has half a tile of padding on average; of many
+        // rounds the last is less than a whole one, as workgroups drift apart).
+        // 16384 x 1024 -> 2048 in 7 uneven groups: 94 us with 192 rows, 103 with 256;
+        // 16384 x 4096 -> 4096 in one group: 603 us with 192, 531 with 256.
+        if constexpr (sizeof(T) == 2) {
+            if (tiles(256, 256) >= 256) {
+                const auto cost = [&](int bm) {
+                    const double rows = a.n_groups == 1 ? (a.n_rows + bm - 1) / bm
+                                                        : double(a.n_rows) / bm + 0.5 * a.n_groups;
+                    const double rounds = rows * ((a.n + 255) / 256) / 256;
+                    return bm * (rounds < 3 ? ceil(rounds) : rounds + 0.5);
+                };
+                if (1.05 * cost(192) < cost(256))
+                    return run<T, 192, 256, 2, 4, 128, 2, WT, true>(a, stream);
+                return run<T, 256, 256, 2, 4, 128, 2, WT, true>(a, stream);
+            }
+        }
         return run<T, 128, 128, 2, 2, 128, 2, WT, true>(a, stream);
     }
     if (bn == 96) return run<T, 128, 96, 4, 1, 128, 2, WT, true>(a, stream);
