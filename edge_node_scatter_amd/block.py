@@ -406,7 +406,7 @@ class AdamW:
             raise ValueError("params is empty")
         if state_bits not in (32, 8):
             raise ValueError("state_bits must be 32 or 8")
-        self.device = self.params[0].device
+        self.device = _typed(self.params[0], "params[0]", torch.float32).device
         self.copies = None if copies is None else list(copies)
         if self.copies is not None and len(self.copies) != len(self.params):
             raise ValueError("copies must be one tensor for each parameter")

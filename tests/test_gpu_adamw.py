@@ -218,6 +218,25 @@ def test_missing_gradients_zero_and_non_finite(dev, bits):
         assert torch.isnan(m1[3][7]) and torch.isfinite(m1[3][:7]).all()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_tensor_past_32_bits(dev, bits):
+    """A tensor of more than 2^31 elements, and one behind it: the last elements move as those of a small tensor do."""
+    say("adamw wide", bits)
+    n = (1 << 31) + 1000
+    tail = torch.randn(5000, generator=torch.Generator().manual_seed(2)).to(dev)
+    p = torch.zeros(n, device=dev)
+    g = torch.zeros(n, dtype=BF16, device=dev)
+    p[-5000:], g[-5000:] = tail, 0.1 * tail.flip(0)
+    q, h = tail.clone(), (0.1 * tail.flip(0)).to(BF16)
+    opt = zs.AdamW([p, q], state_bits=bits, **HP)
+    opt.step([g, h])
+    small = zs.AdamW([tail.clone()], state_bits=bits, **HP)
+    small.step([h])
+    # from zero moments the parameters do not depend on how the moments are held
+    assert torch.equal(p[-5000:], small.params[0]) and torch.equal(q, small.params[0])
+    assert (p[:-5000] == 0).all()
+
+
 def test_state_is_taken_over_and_graph(dev):
     say("adamw state, graph")
     for bits in (32, 8):

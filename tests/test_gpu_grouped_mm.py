@@ -98,6 +98,82 @@ def test_long_groups_are_cut_and_joined(dev, dtype, shape):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(3000, 511, 24, 40), (3000, 513, 24, 40), (5000, 2000, 72, 40), (300, 5000, 8, 136), (6000, 70000, 8, 8)])
+def test_many_groups(dev, dtype, shape):
+    """Around and above the number of groups whose tiles are counted, where a search finds a workgroup's group; more
+    groups than rows; more than a grid's second dimension holds."""
+    M, G, k, n = shape
+    say("many groups", shape, dtype)
+    rng = np.random.default_rng(G)
+    x, w, gy, _, p = make(M, 1, k, n, dtype, True, seed=G)
+    # few long groups among many short and empty ones
+    at = np.sort(np.concatenate([rng.integers(0, M + 1, G - 1), [0, M]]))
+    at[G // 2: G // 2 + G // 8] = at[G // 2]
+    off = torch.from_numpy(at.astype(np.int32))
+    w = torch.randn(1, k, n, generator=torch.Generator().manual_seed(1)).to(dtype).expand(G, k, n)
+    groups = groups_of(off, p, dev)
+    y = zs.zs_grouped_mm(x.to(dev), w.to(dev), groups)
+    one = torch.tensor([0, M], dtype=torch.int32)   # equal weights: as one group
+    ref, s = blockref.grouped(x, w[:1], one, p)
+    close(y, ref, blockref.sum_bound(ref, s, k, dtype), "y")
+    gx, gw = zs.zs_grouped_mm_backward(gy.to(dev), x.to(dev), w.to(dev), groups)
+    ref, s = blockref.grouped(gy, w[:1].transpose(1, 2), one, p)
+    close(gx, ref, blockref.sum_bound(ref, s, n, dtype), "grad_x")
+    live = [g for g in range(G) if at[g + 1] > at[g]]
+    assert (gw[torch.tensor([g for g in range(G) if at[g + 1] == at[g]], device=dev)] == 0).all()
+    for g in live[:: max(1, len(live) // 200)] + [int(np.argmax(np.diff(at)))]:
+        r = blockref.group_rows(off, p, g)
+        ref, s = x[r].double().T @ gy[r].double(), x[r].double().abs().T @ gy[r].double().abs()
+        close(gw[g], ref, blockref.sum_bound(ref, s, M, dtype), f"grad_w[{g}]")
+
+
+def test_tile_shapes_of_large_products(dev):
+    """bf16 products large enough for the tallest tiles, in one group (256 rows) and in uneven ones (192): rows against
+    float64 at the ends of tiles and groups."""
+    for M, G, k, n in ((16600, 1, 256, 4096), (16384, 7, 264, 2048), (9000, 3, 128, 8200)):
+        say("large tiles", M, G, k, n)
+        x, w, gy, off, p = make(M, G, k, n, BF16, True, seed=k, empty=False)
+        y = zs.zs_grouped_mm(x.to(dev), w.to(dev), groups_of(off, p, dev)).cpu()
+        pos = torch.unique(torch.cat([off.long()[:-1], off.long()[1:] - 1, torch.arange(0, M, 191), torch.arange(M - 300, M)]))
+        group = torch.searchsorted(off[1:].long(), pos, right=True)
+        rows = p[pos].long()
+        for g in range(G):
+            r = rows[group == g]
+            ref, s = x[r].double() @ w[g].double(), x[r].double().abs() @ w[g].double().abs()
+            close(y[r], ref, blockref.sum_bound(ref, s, k, BF16), f"group {g}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_offsets_past_32_bits(dev, dtype):
+    """Rows whose elements lie more than 2^32 elements from the start, in x, grad_y and the output, and weights of
+    groups that far apart."""
+    M, G, k, n = 700, 2, 40, 24
+    stride = 1 << 23
+    say("wide offsets", dtype)
+    x, w, gy, off, p = make(M, G, k, n, dtype, True, seed=21, empty=False)
+    groups = groups_of(off, p, dev)
+    size = (M - 1) * stride + 64
+    assert size > 1 << 32
+    big = torch.empty(size, dtype=dtype, device=dev)
+    xv, gv, yv = (big.as_strided((M, c), (stride, 1), at) for c, at in ((k, 0), (n, 0), (n, 0)))
+    ref, s = blockref.grouped(x, w, off, p)
+    xv.copy_(x.to(dev))
+    close(zs.zs_grouped_mm(xv, w.to(dev), groups), ref, blockref.sum_bound(ref, s, k, dtype), "y")
+    gref, gs = blockref.grouped_wgrad(x, gy, off, p, G)
+    close(zs.zs_grouped_mm_backward(gy.to(dev), xv, w.to(dev), groups)[1], gref, blockref.sum_bound(gref, gs, M, dtype), "grad_w")
+    zs.zs_grouped_mm(x.to(dev), w.to(dev), groups, out=yv)
+    close(yv, ref, blockref.sum_bound(ref, s, k, dtype), "y, wide")
+    gv.copy_(gy.to(dev))
+    gx, gw = zs.zs_grouped_mm_backward(gv, x.to(dev), w.to(dev), groups)
+    close(gw, gref, blockref.sum_bound(gref, gs, M, dtype), "grad_w, wide grad_y")
+    xref, xs = blockref.grouped(gy, w.transpose(1, 2), off, p)
+    close(gx, xref, blockref.sum_bound(xref, xs, n, dtype), "grad_x, wide grad_y")
+    far = big.as_strided((G, k, n), (size - k * n, n, 1))
+    far.copy_(w.to(dev))
+    close(zs.zs_grouped_mm(x.to(dev), far, groups), ref, blockref.sum_bound(ref, s, k, dtype), "y, far weights")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("perm", [False, True])
 def test_rows_of_no_group_get_zeros(dev, dtype, perm):
     M, G, k, n = 400, 5, 48, 72

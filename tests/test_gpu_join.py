@@ -232,6 +232,26 @@ def test_strided_views(dev, dtype, pad):
     assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_offsets_past_32_bits(dev, dtype):
+    """Row strides that take rows more than 2^32 elements from the start."""
+    M, c, stride = 260, 64, 1 << 25
+    say("wide offsets", dtype)
+    d, gy, gh = make(M, c, dtype, "full", seed=31)
+    big = torch.empty((M - 1) * stride + c, dtype=dtype, device=dev)
+    assert big.numel() > 1 << 32
+    args = on(d, dev)
+    want = zs.zs_block_join(*args, eps=EPS)
+    back = zs.zs_block_join_backward(gy.to(dev), gh.to(dev), *args, eps=EPS)
+    for i in range(3):
+        view = big.as_strided((M, c), (stride, 1))
+        view.copy_(args[i])
+        wide = [view if j == i else t for j, t in enumerate(args)]
+        assert all(torch.equal(a, b) for a, b in zip(want, zs.zs_block_join(*wide, eps=EPS)))
+        got = zs.zs_block_join_backward(gy.to(dev), gh.to(dev), *wide, eps=EPS)
+        assert all(torch.equal(a, b) for a, b in zip(back, got))
+
+
 def test_autograd_against_differences(dev):
     """block_join and block_norm under autograd: a directional derivative against central differences in float64."""
     say("autograd")
