@@ -103,53 +103,78 @@ __global__ __launch_bounds__(WM * WN * 64) void zs_gmm_kernel(const MmParams<T> 
                 b_ptr[i] = c < BN && b_n[i] < p.n ? w + int64_t(b_k[i]) * p.ldw + b_n[i] : nullptr;
             }
         }
-        // VEC: straight to LDS; otherwise through registers, all loads first
-        const auto load = [&](int k0, char* buf) {
-            u32x4 held[VEC ? 1 : IA + IB];
+        const int stages = (p.k + BK - 1) / BK;
+        const auto read_a = [&](const char* at, int i, int s) {
+            return read_row_frag<T, KB>(at, wm * MT + i, s, lane);
+        };
+        const auto read_b = [&](const char* at, int j, int s) {
+            if constexpr (WT)
+                return read_row_frag<T, KB>(at + kABytes, wn * NT + j, s, lane);
+            else
+                return read_sum_frag<T, LN>(at + kABytes, wn * NT + j, s, lane);
+        };
+        if constexpr (VEC) {
+            const auto load = [&](int stage, char* buf) {
+                const int k0 = stage * BK;
 #pragma unroll
-            for (int i = 0; i < IA; ++i) {
-                const int left = p.k - k0 - a_k[i];
-                const bool in = a_ptr[i] && left > 0;
-                const T* src = a_ptr[i] + k0;
-                if constexpr (VEC)
-                    load_to_lds(in ? static_cast<const void*>(src) : zero_chunk,
+                for (int i = 0; i < IA; ++i) {
+                    const bool in = a_ptr[i] && k0 + a_k[i] < p.k;
+                    load_to_lds(in ? static_cast<const void*>(a_ptr[i] + k0) : zero_chunk,
                                 lds_offset(buf + (wave * IA + i) * 1024));
-                else
-                    held[i] = load_partial(src, in ? left : 0);
-            }
+                }
 #pragma unroll
-            for (int i = 0; i < IB; ++i) {
-                const bool in = b_ptr[i] && k0 + b_k[i] < p.k;
-                const T* src = b_ptr[i] + (WT ? int64_t(k0) : int64_t(k0) * p.ldw);
-                const int left = WT ? p.k - k0 - b_k[i] : p.n - b_n[i];
-                if constexpr (VEC)
+                for (int i = 0; i < IB; ++i) {
+                    const bool in = b_ptr[i] && k0 + b_k[i] < p.k;
+                    const T* src = b_ptr[i] + (WT ? int64_t(k0) : int64_t(k0) * p.ldw);
                     load_to_lds(in ? static_cast<const void*>(src) : zero_chunk,
                                 lds_offset(buf + kABytes + (wave * IB + i) * 1024));
-                else
-                    held[IA + i] = load_partial(src, in ? left : 0);
-            }
-            if constexpr (!VEC) {
+                }
+            };
+            product_loop<T, MT, NT, KB, S, kBytes, IA + IB, false>(
+                stages, lds, acc, load, read_a, read_b, [](int, const char*) {});
+        } else {
+            // S stages at a time through registers, so that their loads' latency is
+            // paid once: all loads, all writes to LDS, then the products (10 rows of 4
+            // groups, 1001 -> 1501 with weights [n][k] in bf16: 21 us with two buffers
+            // in turn, 13 with four stages at a time).  Large products keep one: their
+            // compute units have other workgroups to go on with, and registers for two
+            // stages leave room for fewer (16384 x 1001 -> 2047: 392 and 206 us).
+            for (int first = 0; first < stages; first += S) {
+                u32x4 held[S][IA + IB];
 #pragma unroll
-                for (int i = 0; i < IA; ++i)
-                    *reinterpret_cast<u32x4*>(buf + (wave * IA + i) * 1024 + lane * 16) = held[i];
+                for (int u = 0; u < S; ++u) {
+                    const int k0 = (first + u) * BK;
 #pragma unroll
-                for (int i = 0; i < IB; ++i)
-                    *reinterpret_cast<u32x4*>(buf + kABytes + (wave * IB + i) * 1024 + lane * 16) =
-                        held[IA + i];
+                    for (int i = 0; i < IA; ++i) {
+                        const int left = a_ptr[i] ? p.k - k0 - a_k[i] : 0;
+                        held[u][i] = load_partial(a_ptr[i] + k0, left);
+                    }
+#pragma unroll
+                    for (int i = 0; i < IB; ++i) {
+                        const bool in = b_ptr[i] && k0 + b_k[i] < p.k;
+                        const int left = WT ? p.k - k0 - b_k[i] : p.n - b_n[i];
+                        held[u][IA + i] = load_partial(
+                            b_ptr[i] + (WT ? int64_t(k0) : int64_t(k0) * p.ldw), in ? left : 0);
+                    }
+                }
+                tile_barrier();   // every wavefront is done with the stages before
+#pragma unroll
+                for (int u = 0; u < S; ++u) {
+                    if (u >= stages) break;   // as many buffers as stages at most
+                    char* buf = lds + u * kBytes + lane * 16;
+#pragma unroll
+                    for (int i = 0; i < IA; ++i)
+                        *reinterpret_cast<u32x4*>(buf + (wave * IA + i) * 1024) = held[u][i];
+#pragma unroll
+                    for (int i = 0; i < IB; ++i)
+                        *reinterpret_cast<u32x4*>(buf + kABytes + (wave * IB + i) * 1024) =
+                            held[u][IA + i];
+                }
+                tile_barrier();
+                for (int u = 0; u < S && first + u < stages; ++u)
+                    multiply_stage<T, MT, NT, KB>(lds + u * kBytes, acc, read_a, read_b);
             }
-        };
-        product_loop<T, MT, NT, KB, S, kBytes, IA + IB, false>(
-            (p.k + BK - 1) / BK, lds, acc, [&](int i, char* buf) { load(i * BK, buf); },
-            [&](const char* at, int i, int s) {
-                return read_row_frag<T, KB>(at, wm * MT + i, s, lane);
-            },
-            [&](const char* at, int j, int s) {
-                if constexpr (WT)
-                    return read_row_frag<T, KB>(at + kABytes, wn * NT + j, s, lane);
-                else
-                    return read_sum_frag<T, LN>(at + kABytes, wn * NT + j, s, lane);
-            },
-            [](int, const char*) {});
+        }
     }
 
     const bool wide = p.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(p.y) % (4 * sizeof(T)) == 0;
@@ -201,8 +226,8 @@ hipError_t dispatch(const GmmArgs& a, hipStream_t stream) {
         return (a.n_rows / bm + a.n_groups) * ((a.n + bn - 1) / bn);
     };
     const bool few = tiles(128, 128) < 256;
-    if (!vec && !few && a.n > 64) return run<T, 128, 128, 2, 2, 128, 2, WT, false>(a, stream);
-    if (!vec) return run<T, 64, 64, 2, 2, 128, 2, WT, false>(a, stream);
+    if (!vec && !few && a.n > 64) return run<T, 128, 128, 2, 2, 128, 1, WT, false>(a, stream);
+    if (!vec) return run<T, 64, 64, 2, 2, 128, 4, WT, false>(a, stream);
     // tiles too few for the compute units: smaller ones, more stages in flight
     if (few) return run<T, 32, 64, 2, 2, 128, 4, WT, true>(a, stream);
     const int bn = tile_side(a.n, true);

@@ -174,7 +174,7 @@ __device__ inline u32x4 load_partial(const T* p, int count) {
     u.v = u32x4{0, 0, 0, 0};
     if (count >= E) {
         __builtin_memcpy(&u.v, p, 16);
-    } else {
+    } else if (count > 0) {
 #pragma unroll
         for (int j = 0; j < E; ++j)
             if (j < count) u.e[j] = p[j];
@@ -203,12 +203,32 @@ __device__ inline void store4(T* p, f32x4 v) {
     }
 }
 
+// The products of one stage; read_a(buf, i, s) and read_b(buf, j, s) read the
+// fragments of its sub-stage s.
+template <typename T, int MT, int NT, int KB, typename ReadA, typename ReadB>
+__device__ inline void multiply_stage(const char* at, f32x4 (&acc)[MT][NT], ReadA read_a,
+                                      ReadB read_b) {
+    using V = typename Frag<T>::V;
+#pragma unroll
+    for (int s = 0; s < KB / 64; ++s) {
+        V a[MT], b[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) b[j] = read_b(at, j, s);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) a[i] = read_a(at, i, s);
+#pragma unroll
+        for (int step = 0; step < mma_steps<T>(); ++step)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) acc[i][j] = mma_step(b[j], a[i], acc[i][j], step);
+    }
+}
+
 // The product loop over `stages` stages, S buffers of kBytes deep.  issue(i, buf)
-// starts the loads of stage i (kLoads per wavefront); read_a(buf, i, s) and
-// read_b(buf, j, s) read fragments of sub-stage s; also(i, buf) does what else a
-// stage is for.  One barrier a stage: it
-// publishes the stage and says that every wavefront is done with the one before,
-// whose buffer the next loads fill.  (Reading the fragments of the next sub-stage
+// starts the loads of stage i (kLoads per wavefront); also(i, buf) does what else
+// a stage is for.  One barrier a stage: it publishes the stage and says that every
+// wavefront is done with the one before, whose buffer the next loads fill.  (Reading the fragments of the next sub-stage
 // ahead, across the barrier, was no faster in the products and slower in the
 // weight gradient, whose transposed reads then crowd its registers: 16384 x
 // 4096 x 4096 in bf16 495 us either way, its weight gradient 680 and 775.)
@@ -220,8 +240,6 @@ template <typename T, int MT, int NT, int KB, int S, int kBytes, int kLoads, boo
           typename Issue, typename ReadA, typename ReadB, typename Also>
 __device__ inline void product_loop(int stages, char* lds, f32x4 (&acc)[MT][NT], Issue issue,
                                     ReadA read_a, ReadB read_b, Also also) {
-    using V = typename Frag<T>::V;
-    constexpr int NS = KB / 64;
     if (stages <= 0) return;
 #pragma unroll
     for (int i = 0; i < S - 1; ++i)
@@ -240,21 +258,7 @@ __device__ inline void product_loop(int stages, char* lds, f32x4 (&acc)[MT][NT],
         const char* at = lds + cur * kBytes;
         if (stage + S - 1 < stages) issue(stage + S - 1, lds + (cur == 0 ? S - 1 : cur - 1) * kBytes);
         cur = cur + 1 == S ? 0 : cur + 1;
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            V a[MT], b[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) b[j] = read_b(at, j, s);
-#pragma unroll
-            for (int i = 0; i < MT; ++i) a[i] = read_a(at, i, s);
-#pragma unroll
-            for (int step = 0; step < mma_steps<T>(); ++step)
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        acc[i][j] = mma_step(b[j], a[i], acc[i][j], step);
-        }
+        multiply_stage<T, MT, NT, KB>(at, acc, read_a, read_b);
         also(stage, at);
     }
 }
