@@ -23,6 +23,10 @@ contiguous tensors (``zs_forward_strided`` / ``zs_backward_strided``).
 ``gie_zonal_scatter_normalized(coupling, radial, env, csr)`` adds the
 inverse-square-root degree normalisation that follows the scatter on the same
 page ("What", third bullet), with the envelope gradient it carries.
+
+``edge_node_scatter_amd.block`` binds the learned operators around the scatter
+(``grouped_mm``, ``block_join``, ``block_norm``, ``AdamW`` and the functions
+under them); they are imported here too.
 """
 from __future__ import annotations
 

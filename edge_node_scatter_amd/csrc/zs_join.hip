@@ -14,6 +14,14 @@
 // wavefront, LDS).  The parameter gradients are summed over a workgroup's rows
 // in registers, then over its row slots in LDS, and the workgroups' partial
 // sums are added in order by a second kernel.
+//
+// Bound by memory.  Measured on MI355X (a copy reaches 5.1 TB/s):
+//  - gradients of 32768 x 2048 in bf16: 242 us and 5 us for the partial sums, 4.4 TB/s
+//    of 1.07 GB; some 60 vector instructions an element beside them (a workgroup a
+//    row, a chunk a lane, the next row's loads in flight; without those 363 us).
+//  - gradients of 16384 x 520 in fp32: 44 and 4 us, 4.6 TB/s of 205 MB (130 chunks of
+//    a wavefront's 192).
+//  - forward of 65536 x 32 in fp32: 9.7 us, 4.3 TB/s of 42 MB.
 #include "zs_block_internal.h"
 #include "zs_tile.h"
 
@@ -178,8 +186,9 @@ struct JoinParams {
 
 // The calls that training makes (all inputs and outputs there, everything on 16
 // bytes) have code of their own without tests: a gate per channel, a gate per
-// row.  Any takes the rest by the parameters.  With the tests in the element
-// loops the gradients of 32768 x 2048 in bf16 took 291 us.
+// row.  kAny takes the rest by the parameters.  With the tests in the element
+// loops, and lane sums through LDS, the gradients of 32768 x 2048 in bf16 took 291
+// us and not 247, those of 16384 x 520 in fp32 92 and not 51.
 enum Mode { kAny, kFull, kRow };
 template <Mode M, typename T>
 __device__ inline bool has_z(const JoinParams<T>& p) {

@@ -263,6 +263,10 @@ __device__ inline void product_loop(int stages, char* lds, f32x4 (&acc)[MT][NT],
     }
 }
 
+// Width of an LDS tile's rows for `v` kept indices: a wavefront's load covers whole
+// rows.
+constexpr int pow2_at_least(int v) { return v <= 32 ? 32 : v <= 64 ? 64 : v <= 128 ? 128 : 256; }
+
 // Side of the tiles that cover `width`: as few tiles as sides of 128 need, as
 // narrow as covers it, so that little of a tile is padding while wide operands
 // are still read as few times as 128 allows.

@@ -2,7 +2,7 @@
 // grad_w[g] = sum over the rows i of group g of x[i]^T grad_y[i].
 //
 // The summed index is the row, so both operands lie in LDS in sum form and are
-// read transposed.  A workgroup forms a BK x BN tile of one piece (at most
+// read transposed.  A workgroup forms a BA x BN tile of one piece (at most
 // `piece` rows) of one group.  A group of one piece is written at once; the
 // pieces of a longer one leave fp32 partial sums that a second kernel adds in
 // order.
@@ -10,6 +10,18 @@
 // Narrow weights (one tile, which the wavefronts also hold as fragments): the
 // same pass forms grad_x[i] = grad_y[i] w[g]^T from the rows of grad_y that lie in
 // LDS for the weight gradient, so that they are read once.
+//
+// Measured on MI355X:
+//  - 647170 rows, 14 uneven groups of 16, 32 -> 96, fp32, perm, both gradients:
+//    100 us and 5 us for the partial sums, 3.9 TB/s of the 417 MB that have to move
+//    (81 us at a copy's rate); the weight gradient alone 66 us, at a copy's rate.
+//    The fp32 matrix instructions (48 a wavefront and stage) are 50 us of it and
+//    overlap the loads only in part.
+//  - 8191 rows, 14 uneven groups of 16, 776 x 1160, bf16: 46 us and 7 us for the
+//    partial sums.  Bound by the start and end of its short work items (7 stages on
+//    average, two and a half rounds of them) and by what the longest group leaves.
+//  - 16384 rows, one group, 4096 x 4096, bf16: 680 us, 810 TFLOP/s; two transposed
+//    LDS reads feed each matrix instruction's operand.
 #include "zs_block_internal.h"
 #include "zs_tile.h"
 
@@ -45,7 +57,6 @@ __device__ inline int64_t clamp_offset(const int32_t* offsets, int64_t v, int64_
 // pieces of cut groups never meet and end by floor(2 n_rows / piece).
 __device__ inline int64_t first_piece(int64_t start, int64_t piece) { return 2 * start / piece; }
 
-constexpr int pow2_at_least(int v) { return v <= 32 ? 32 : v <= 64 ? 64 : 128; }
 constexpr int kIndexRows = 1024;   // row indices kept in LDS at a time
 
 // VEC as in the grouped products.  BOTH: grad_x too; k <= BA and n <= BN.
@@ -340,7 +351,7 @@ hipError_t run(WgParams<T> p, hipStream_t stream) {
     p.spread = p.k_tiles * p.n_tiles >= 16 && p.n_groups <= kCountedGroups;
     const int64_t slots = p.n_rows / p.piece + p.n_groups + (BOTH ? 2 : 0);
     const int64_t grid = work_grid(slots, int64_t(p.k_tiles) * p.n_tiles, p.spread);
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;   // operands far above 288 GB
     const int64_t longest = p.piece < p.n_rows ? p.piece : p.n_rows;
     const int stages = int((longest + BR - 1) / BR);
     const int bytes = (stages < 1 ? 1 : stages < S ? stages : S) * (BA + pow2_at_least(BN)) * KB;
