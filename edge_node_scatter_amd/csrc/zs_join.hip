@@ -16,10 +16,10 @@
 // sums are added in order by a second kernel.
 //
 // Bound by memory.  Measured on MI355X (a copy reaches 5.1 TB/s):
-//  - gradients of 32768 x 2048 in bf16: 242 us and 5 us for the partial sums, 4.4 TB/s
+//  - gradients of 32768 x 2048 in bf16: 236 us and 5 us for the partial sums, 4.5 TB/s
 //    of 1.07 GB; some 60 vector instructions an element beside them (a workgroup a
 //    row, a chunk a lane, the next row's loads in flight; without those 363 us).
-//  - gradients of 16384 x 520 in fp32: 44 and 4 us, 4.6 TB/s of 205 MB (130 chunks of
+//  - gradients of 16384 x 520 in fp32: 42 and 4 us, 4.9 TB/s of 205 MB (130 chunks of
 //    a wavefront's 192).
 //  - forward of 65536 x 32 in fp32: 9.7 us, 4.3 TB/s of 42 MB.
 #include "zs_block_internal.h"
@@ -58,18 +58,28 @@ struct Chunk {
     }
 };
 
-// Chunk `chunk` of a row of c elements (zeros outside).
-template <typename T>
+// Chunk `chunk` of a row of c elements (zeros outside).  vec: whole chunks on 16
+// bytes; NT: read once, past the caches.
+template <typename T, bool NT = false>
 __device__ inline u32x4 load_chunk(const T* row, int chunk, int c, bool vec) {
     constexpr int V = Chunk<T>::V;
     const int left = c - chunk * V;
+    if (NT && vec)
+        return left > 0
+                   ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + chunk * V))
+                   : u32x4{0, 0, 0, 0};
     if (vec) return left > 0 ? *reinterpret_cast<const u32x4*>(row + chunk * V) : u32x4{0, 0, 0, 0};
     return load_partial(row + chunk * V, left);
 }
 template <typename T>
-__device__ inline void store_chunk(T* row, int chunk, int c, bool vec, u32x4 v) {
+__device__ inline void store_chunk(T* row, int chunk, int c, bool vec, u32x4 v,
+                                   bool stream = false) {
     constexpr int V = Chunk<T>::V;
     const int left = c - chunk * V;
+    if (vec && stream) {
+        if (left > 0) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(row + chunk * V));
+        return;
+    }
     if (vec) {
         if (left > 0) *reinterpret_cast<u32x4*>(row + chunk * V) = v;
         return;
@@ -178,6 +188,7 @@ struct JoinParams {
     int c, gate_kind;   // 0: none, 1: one per row, 2: one per channel
     float eps, inv_c;
     bool vec;
+    bool stream;   // the backward's outputs go past the caches
     T *y, *h;
     const T *gy, *gh;
     T *gx, *gz, *ggate;
@@ -312,11 +323,11 @@ __device__ inline RowInputs<NV> load_row(const JoinParams<T>& p, int64_t row, in
         const int at = l + j * L;
         r.z[j] = r.x[j] = r.gate[j] = r.gy[j] = r.gh[j] = zero;
         if (at * Chunk<T>::V < c) {
-            r.x[j] = load_chunk(p.x + row * p.ldx, at, c, vec);
-            if (has_z<M>(p)) r.z[j] = load_chunk(p.z + row * p.ldz, at, c, vec);
-            if (gate_of<M>(p) == 2) r.gate[j] = load_chunk(p.gate + row * p.ldg, at, c, vec);
-            if (M != kAny || p.gy) r.gy[j] = load_chunk(p.gy + row * p.c, at, c, vec);
-            if (M != kAny || p.gh) r.gh[j] = load_chunk(p.gh + row * p.c, at, c, vec);
+            r.x[j] = load_chunk<T, true>(p.x + row * p.ldx, at, c, vec);
+            if (has_z<M>(p)) r.z[j] = load_chunk<T, true>(p.z + row * p.ldz, at, c, vec);
+            if (gate_of<M>(p) == 2) r.gate[j] = load_chunk<T, true>(p.gate + row * p.ldg, at, c, vec);
+            if (M != kAny || p.gy) r.gy[j] = load_chunk<T, true>(p.gy + row * p.c, at, c, vec);
+            if (M != kAny || p.gh) r.gh[j] = load_chunk<T, true>(p.gh + row * p.c, at, c, vec);
         }
     }
     r.row_gate = gate_of<M>(p) == 1 && live ? float(p.gate[row * p.ldg]) : 0.0f;
@@ -418,7 +429,7 @@ __global__ __launch_bounds__(threads_of(L), (resident<T, L, NV, M>())) void zs_j
                     gx[j][i] = __builtin_fmaf(ry, gh[i] * w[i], gx[j][i]) - my * y[j][i];
                 }
             }
-            if (live) store_chunk(p.gx + row * p.c, at, c, vec_of<M>(p), Chunk<T>::pack(gx[j]));
+            if (live) store_chunk(p.gx + row * p.c, at, c, vec_of<M>(p), Chunk<T>::pack(gx[j]), p.stream);
             if (has_z<M>(p)) {
                 float z[V], a[V], sc[V], wp[V], ga[V];
                 Chunk<T>::unpack(in.z[j], z);
@@ -439,7 +450,7 @@ __global__ __launch_bounds__(threads_of(L), (resident<T, L, NV, M>())) void zs_j
                     gx[j][i] = r;
                 }
                 if (gate_of<M>(p) == 2 && live)
-                    store_chunk(p.ggate + row * p.c, at, c, vec_of<M>(p), Chunk<T>::pack(ga));
+                    store_chunk(p.ggate + row * p.c, at, c, vec_of<M>(p), Chunk<T>::pack(ga), p.stream);
             }
         }
         if (has_z<M>(p)) {
@@ -452,7 +463,7 @@ __global__ __launch_bounds__(threads_of(L), (resident<T, L, NV, M>())) void zs_j
                 Chunk<T>::unpack(in.z[j], z);
 #pragma unroll
                 for (int i = 0; i < V; ++i) z[i] = rz * (gx[j][i] - z[i] * rz * mz);
-                if (live) store_chunk(p.gz + row * p.c, l + j * L, c, vec_of<M>(p), Chunk<T>::pack(z));
+                if (live) store_chunk(p.gz + row * p.c, l + j * L, c, vec_of<M>(p), Chunk<T>::pack(z), p.stream);
             }
         }
     }
@@ -526,6 +537,12 @@ JoinParams<T> params(const JoinArgs& a) {
     p.vec = a.c % V == 0 && a.ldx % V == 0 && on16(a.x) && on16(a.y) && on16(a.h) && on16(a.gy) &&
             on16(a.gh) && on16(a.gx) && on16(a.gz) && on16(a.scale) && on16(a.w_post) &&
             on16(a.w_pre);
+    // Gradients that fill half of the memory-side cache by themselves are written past
+    // the caches (32768 x 2048 in bf16, 134 MB each: 240 us, 246 otherwise); smaller
+    // ones are there for whoever reads them next (16384 x 520 in fp32, 34 MB: 49 past
+    // the caches, 48 otherwise).  The backward's inputs, read once, are always read
+    // past them (247 and 51 us otherwise).
+    p.stream = a.n_rows * a.c * int64_t(sizeof(T)) >= (int64_t(128) << 20);
     if (a.z) p.vec = p.vec && a.ldz % V == 0 && on16(a.z);
     if (p.gate_kind == 2)
         p.vec = p.vec && a.ldg % V == 0 && on16(a.gate) && on16(a.ggate);
