@@ -327,24 +327,30 @@ def zs_block_join_backward(grad_y: torch.Tensor | None, grad_h: torch.Tensor | N
     """(grad_x, grad_z, grad_gate, grad_scale, grad_w_post, grad_w_pre), None
     for inputs that are None.  grad_y or grad_h may be None (zeros)."""
     x, z, gate, scale, w_post, w_pre = _join_inputs(x, z, gate, scale, w_post, w_pre)
-    dev, (M, c) = x.device, x.shape
+    dev, shape, (M, c) = x.device, x.shape, x.shape
     for name, g in (("grad_y", grad_y), ("grad_h", grad_h)):
-        if g is not None:
+        if g is not None and not (g.dtype == x.dtype and g.device == dev and g.shape == shape):
             _typed(g, name, x.dtype, dev)
-            if g.shape != x.shape:
-                raise ValueError(f"{name} must have x's shape")
-    grad_y = None if grad_y is None else grad_y.contiguous()
-    grad_h = None if grad_h is None else grad_h.contiguous()
-    like = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=dev)  # noqa: E731
-    grads = [like(t) for t in (x, z, gate, scale, w_post, w_pre)]
+            raise ValueError(f"{name} must have x's shape")
+    grad_y = grad_y if grad_y is None or grad_y.is_contiguous() else grad_y.contiguous()
+    grad_h = grad_h if grad_h is None or grad_h.is_contiguous() else grad_h.contiguous()
+    gx = x.new_empty(shape)
+    gz = None if z is None else x.new_empty(shape)
+    gg = None if gate is None else x.new_empty(gate.shape)
+    # the parameters' gradients in one allocation
+    gs, gpost, gpre = torch.empty((3, c), dtype=torch.float32, device=dev).unbind(0)
+    if z is None:
+        gs = gpost = None
+    if w_pre is None:
+        gpre = None
     lib = load_block()
     size = lib.zs_block_join_workspace_bytes(M, c)
     ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
     _check("zs_block_join_backward", _call(
         dev, lib.zs_block_join_backward, _ptr(grad_y), _ptr(grad_h),
-        *_join_args(x, z, gate, scale, w_post, w_pre, eps), *(_ptr(g) for g in grads), _ptr(ws),
-        size))
-    return tuple(grads)
+        *_join_args(x, z, gate, scale, w_post, w_pre, eps), _ptr(gx), _ptr(gz), _ptr(gg),
+        _ptr(gs), _ptr(gpost), _ptr(gpre), _ptr(ws), size))
+    return gx, gz, gg, gs, gpost, gpre
 
 
 class _BlockJoin(torch.autograd.Function):

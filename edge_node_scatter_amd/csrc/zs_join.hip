@@ -467,10 +467,12 @@ __global__ __launch_bounds__(threads_of(L), (resident<T, L, NV, M>())) void zs_j
             }
         }
     }
-    // sums over the workgroup's row slots, then out: [3][c] per workgroup
-    float* out = p.partial + int64_t(blockIdx.x) * 3 * p.c;
+    // sums over the workgroup's row slots, then out: [3][c] per workgroup; a single
+    // workgroup's are the gradients
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
+        float* out = p.partial + (int64_t(blockIdx.x) * 3 + q) * p.c;
+        if (gridDim.x == 1) out = q == 0 ? p.gscale : (q == 1 ? p.gpost : p.gpre);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             if constexpr (kRowsOf > 1) {
@@ -482,13 +484,13 @@ __global__ __launch_bounds__(threads_of(L), (resident<T, L, NV, M>())) void zs_j
                     const int ch = j * L * V + e;
                     float s = 0.0f;
                     for (int k = 0; k < kRowsOf; ++k) s += sums[k * L * V + e];
-                    if (ch < p.c) out[int64_t(q) * p.c + ch] = s;
+                    if (ch < p.c && out) out[ch] = s;
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const int ch = (j * L + l) * V + i;
-                    if (ch < p.c) out[int64_t(q) * p.c + ch] = acc[q][j][i];
+                    if (ch < p.c && out) out[ch] = acc[q][j][i];
                 }
             }
         }
@@ -567,7 +569,7 @@ hipError_t run_mode(const JoinParams<T>& p, bool backward, hipStream_t stream) {
     if (grid > 0) {
         zs_join_bwd_kernel<T, L, NV, M><<<grid, threads_of(L), 0, stream>>>(p);
         const hipError_t err = hipGetLastError();
-        if (err != hipSuccess) return err;
+        if (err != hipSuccess || grid == 1) return err;
     }
     zs_join_sum_kernel<<<(3 * p.c + 31) / 32, 1024, 0, stream>>>(p.partial, int(grid), p.c,
                                                                  p.gscale, p.gpost, p.gpre);
@@ -616,6 +618,7 @@ hipError_t dispatch(const JoinArgs& a, bool backward, hipStream_t stream) {
 }  // namespace
 
 size_t join_workspace(int64_t n_rows, int64_t c) {
+    if (n_rows == 1) return 0;   // one workgroup
     int64_t parts = n_rows < kMaxPartials ? n_rows : kMaxPartials;
     return size_t(parts * 3 * c * 4);
 }
