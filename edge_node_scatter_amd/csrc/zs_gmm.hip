@@ -191,6 +191,35 @@ __global__ __launch_bounds__(WM * WN * 64) void zs_gmm_kernel(const MmParams<T> 
         }
     }
 
+    // bf16 rows of y on 16 bytes go through LDS as whole lines (16384 x 1024 -> 2048:
+    // 94 us straight from the accumulators, 85 so; 50182 x 128 -> 1328: 69 and 58).
+    // fp32 stores from the accumulators fill 64 bytes of a row and are as fast.
+    if constexpr (sizeof(T) == 2) {
+        using Out = RowsOut<NT>;
+        static_assert(kWaves * Out::kBytes <= kBytes, "results fit the buffer of one stage");
+        if (p.ldy % E == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0) {
+            tile_barrier();   // every wavefront is done with the operands
+            char* mine = lds + wave * Out::kBytes;
+            const int first_n = n0 + wn * NT * 16;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                // a row's number is below 2^31
+                const int row = int(row_at((wm * MT + i) * 16 + (lane & 15)));
+                Out::write(mine, acc[i], lane);
+                wave_lds_sync();
+#pragma unroll
+                for (int t = 0; t < Out::kTurns; ++t) {
+                    const int id = t * 64 + lane;
+                    const int64_t r = __shfl(row, id / Out::kChunks, 64);
+                    const int n = first_n + id % Out::kChunks * E;
+                    if (r >= 0 && n < p.n)
+                        store_partial(p.y + r * p.ldy + n, Out::read(mine, id), p.n - n);
+                }
+                wave_lds_sync();
+            }
+            return;
+        }
+    }
     const bool wide = p.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(p.y) % (4 * sizeof(T)) == 0;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -250,8 +279,8 @@ hipError_t dispatch(const GmmArgs& a, hipStream_t stream) {
         // compute unit; of 256 rows, or of 192 where their last round of workgroups
         // leaves less idle (a group has half a tile of padding on average; of many
         // rounds the last is less than a whole one, as workgroups drift apart).
-        // 16384 x 1024 -> 2048 in 7 uneven groups: 94 us with 192 rows, 103 with 256;
-        // 16384 x 4096 -> 4096 in one group: 603 us with 192, 531 with 256.
+        // 16384 x 1024 -> 2048 in 7 uneven groups: 95 us with 192 rows, 108 with 256;
+        // 16384 x 4096 -> 4096 in one group: 596 us with 192, 543 with 256.
         if constexpr (sizeof(T) == 2) {
             if (tiles(256, 256) >= 256) {
                 const auto cost = [&](int bm) {

@@ -277,6 +277,49 @@ inline int tile_side(int64_t width, bool with96) {
     return 128;
 }
 
+// A wavefront's 16 x (16 NT) results of one row of tiles in bf16, through its part
+// of the LDS (16 rows of kRowBytes), so that stores write whole lines: straight from
+// the accumulators a store instruction covers 32 bytes of each of 16 rows.  write()
+// puts the results there, read() returns the 16-byte chunk `id` (row id / kChunks).
+// Chunks are rotated within their row against bank conflicts.
+template <int NT>
+struct RowsOut {
+    static constexpr int kRowBytes = NT * 32, kChunks = NT * 2, kTurns = NT / 2;
+    static constexpr int kBytes = 16 * kRowBytes;
+    static_assert(NT % 2 == 0, "a store takes 64 chunks");
+    __device__ static char* at(char* lds, int row, int chunk) {
+        const int turn = kRowBytes >= 256 ? row : (kRowBytes == 128 ? row >> 1 : row >> 2);
+        return lds + row * kRowBytes + (chunk + turn) % kChunks * 16;
+    }
+    __device__ static void write(char* lds, const f32x4 (&acc)[NT], int lane) {
+        const int row = lane & 15, q = lane >> 4;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            store4(reinterpret_cast<__bf16*>(at(lds, row, 2 * j + q / 2) + q % 2 * 8), acc[j]);
+    }
+    __device__ static u32x4 read(char* lds, int id) {
+        return *reinterpret_cast<const u32x4*>(at(lds, id / kChunks, id % kChunks));
+    }
+};
+
+// The first `count` values of a 16-byte chunk, to an address on 16 bytes.
+template <typename T>
+__device__ inline void store_partial(T* p, u32x4 v, int count) {
+    constexpr int E = 16 / sizeof(T);
+    if (count >= E) {
+        *reinterpret_cast<u32x4*>(p) = v;
+        return;
+    }
+    union {
+        u32x4 v;
+        T e[E];
+    } u;
+    u.v = v;
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        if (j < count) p[j] = u.e[j];
+}
+
 // ---- ragged groups ------------------------------------------------------------
 // The tiles of ragged groups are numbered without the host reading the offsets:
 // the grid holds as many workgroups as there can be tiles (one part-filled tile

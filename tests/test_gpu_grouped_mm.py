@@ -205,6 +205,24 @@ def test_no_rows(dev):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("size", [(130, 3, 16, 33, 40), (130, 3, 16, 36, 44), (700, 3, 40, 93, 96), (9000, 4, 64, 1021, 1024),
+                                  (9000, 2, 64, 2041, 2056), (33, 2, 24, 7, 8)])
+@pytest.mark.parametrize("perm", [False, True])
+def test_odd_widths_into_padded_rows(dev, dtype, size, perm):
+    """Columns that end inside 16 bytes of a row that starts on 16 bytes: the padding behind them, rows of no group
+    and the rows around the output."""
+    M, G, k, n, stride = size
+    say("padded rows", dtype, size, perm)
+    x, w, gy, off, p = make(M, G, k, n, dtype, perm, seed=n, outside=True)
+    ob = torch.full((M + 2, stride), 77.0, dtype=dtype, device=dev)
+    y = zs.zs_grouped_mm(x.to(dev), w.transpose(1, 2).contiguous().to(dev).transpose(1, 2), groups_of(off, p, dev),
+                         out=ob[1:-1, :n])
+    ref, s = blockref.grouped(x, w, off, p)
+    close(y, ref, blockref.sum_bound(ref, s, k, dtype), "y")
+    assert (ob[0] == 77).all() and (ob[-1] == 77).all() and (ob[:, n:] == 77).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("pad", [1, 8])
 def test_strided_views_and_guards(dev, dtype, pad):
     """Row-strided x and grad_y (aligned and unaligned strides and starts) read in place, a strided output whose
