@@ -467,12 +467,13 @@ __global__ __launch_bounds__(threads_of(L), (resident<T, L, NV, M>())) void zs_j
             }
         }
     }
-    // sums over the workgroup's row slots, then out: [3][c] per workgroup; a single
-    // workgroup's are the gradients
+    // sums over the workgroup's row slots, then out: [3][c] per workgroup.  A single
+    // workgroup's are the gradients (not where a workgroup takes a row at a time: that
+    // would be one row, and the choice costs those kernels spilled registers).
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
         float* out = p.partial + (int64_t(blockIdx.x) * 3 + q) * p.c;
-        if (gridDim.x == 1) out = q == 0 ? p.gscale : (q == 1 ? p.gpost : p.gpre);
+        if (kRowsOf > 1 && gridDim.x == 1) out = q == 0 ? p.gscale : (q == 1 ? p.gpost : p.gpre);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             if constexpr (kRowsOf > 1) {
@@ -569,7 +570,7 @@ hipError_t run_mode(const JoinParams<T>& p, bool backward, hipStream_t stream) {
     if (grid > 0) {
         zs_join_bwd_kernel<T, L, NV, M><<<grid, threads_of(L), 0, stream>>>(p);
         const hipError_t err = hipGetLastError();
-        if (err != hipSuccess || grid == 1) return err;
+        if (err != hipSuccess || (rows > 1 && grid == 1)) return err;
     }
     zs_join_sum_kernel<<<(3 * p.c + 31) / 32, 1024, 0, stream>>>(p.partial, int(grid), p.c,
                                                                  p.gscale, p.gpost, p.gpre);
@@ -618,7 +619,6 @@ hipError_t dispatch(const JoinArgs& a, bool backward, hipStream_t stream) {
 }  // namespace
 
 size_t join_workspace(int64_t n_rows, int64_t c) {
-    if (n_rows == 1) return 0;   // one workgroup
     int64_t parts = n_rows < kMaxPartials ? n_rows : kMaxPartials;
     return size_t(parts * 3 * c * 4);
 }
