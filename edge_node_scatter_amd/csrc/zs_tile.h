@@ -228,10 +228,11 @@ __device__ inline void multiply_stage(const char* at, f32x4 (&acc)[MT][NT], Read
 // The product loop over `stages` stages, S buffers of kBytes deep.  issue(i, buf)
 // starts the loads of stage i (kLoads per wavefront); also(i, buf) does what else
 // a stage is for.  One barrier a stage: it publishes the stage and says that every
-// wavefront is done with the one before, whose buffer the next loads fill.  (Reading the fragments of the next sub-stage
-// ahead, across the barrier, was no faster in the products and slower in the
-// weight gradient, whose transposed reads then crowd its registers: 16384 x
-// 4096 x 4096 in bf16 495 us either way, its weight gradient 680 and 775.)
+// wavefront is done with the one before, whose buffer the next loads fill.
+// (Reading the fragments of the next sub-stage ahead, across the barrier, was no
+// faster in the products and slower in the weight gradient, whose transposed reads
+// then crowd its registers: 16384 x 4096 x 4096 in bf16 495 us either way, its
+// weight gradient 680 and 775.)
 //
 // LATE (S = 2): also() stores, and stores count as loads do; so it is also()
 // that waits for the next stage's loads, before it stores, and the stores have
