@@ -1,13 +1,16 @@
 // The gated residual join between two norms and its gradients, gfx950.
 //
 //   u = zn w_post, zn = z rz, rz = (mean z^2 + eps)^(-1/2)
-//   y = x + scale s u, s = sigmoid(gate);  h = y ry w_pre, ry likewise
+//   y = x + scale s u, s = sigmoid(gate);  h = yn w_pre, yn = y ry, ry likewise
 //
 // backward, with t = gh w_pre and everything recomputed from the inputs:
-//   gx = gy + ry t - y ry^3 mean(t y)
+//   gx = gy + ry (t - yn mean(t yn))
 //   b = gx s, q = b scale, r = q w_post
 //   gz = rz (r - zn mean(r zn)),  ggate = q u (1 - s)
-//   gscale = sum b u, gpost = sum q zn, gpre = sum gh y ry   (over the rows)
+//   gscale = sum b u, gpost = sum q zn, gpre = sum gh yn   (over the rows)
+//
+// No power of ry or rz is formed: a cube leaves fp32's range where the row's norm is
+// under 1e-13 or above 1e13, and times the zero lanes of absent rows it would be NaN.
 //
 // One pass over memory: a row stays in the registers of L lanes, which hold its
 // 16-byte chunks l, l + L, ...; the row sums cross the lanes (and, above a
@@ -407,11 +410,11 @@ __global__ __launch_bounds__(threads_of(L), (resident<T, L, NV, M>())) void zs_j
                 }
             }
         }
-        float ry = 0.0f, my = 0.0f;   // my = ry^3 mean(t y)
+        float ry = 0.0f, my = 0.0f;   // my = mean(t yn)
         if (has_pre<M>(p)) {
             row_sum<L>(s2, lds, region);
             ry = 1.0f / sqrtf(__builtin_fmaf(s2[0], p.inv_c, p.eps));
-            my = ry * ry * ry * (s2[1] * p.inv_c);
+            my = ry * (s2[1] * p.inv_c);
         }
         float s3[2] = {0.0f, 0.0f};   // r zn, q u (1 - s)
         float gx[NV][V];
@@ -425,8 +428,9 @@ __global__ __launch_bounds__(threads_of(L), (resident<T, L, NV, M>())) void zs_j
                 load_param<V>(p.w_pre, at, c, vec_of<M>(p), w);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    acc[2][j][i] = __builtin_fmaf(gh[i] * ry, y[j][i], acc[2][j][i]);
-                    gx[j][i] = __builtin_fmaf(ry, gh[i] * w[i], gx[j][i]) - my * y[j][i];
+                    const float yn = y[j][i] * ry;
+                    acc[2][j][i] = __builtin_fmaf(gh[i], yn, acc[2][j][i]);
+                    gx[j][i] = __builtin_fmaf(ry, gh[i] * w[i], gx[j][i]) - (my * ry) * yn;
                 }
             }
             if (live) store_chunk(p.gx + row * p.c, at, c, vec_of<M>(p), Chunk<T>::pack(gx[j]), p.stream);

@@ -320,3 +320,48 @@ def test_refusals(dev):
         zs.zs_block_join(wide, None, None, None, None, torch.ones(8193, device=dev))
     with pytest.raises(ValueError):
         zs.zs_block_join_backward(gy.to(dev)[:2], None, x, z, gate, scale, post, pre)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate", [None, "row", "full"])
+@pytest.mark.parametrize("shape", [(5, 16), (37, 48), (300, 57), (301, 264), (6, 520), (37, 1032), (3, 4100)])
+def test_small_eps(dev, dtype, gate, shape):
+    """eps = 1e-30: rows of zeros in x, in z and in both, whose norms' factor is 1e15, among ordinary rows, and row
+    counts that leave the last workgroup part empty."""
+    M, c = shape
+    say("small eps", M, c, dtype, gate)
+    d, gy, gh = make(M, c, dtype, gate, seed=M + c)
+    d["x"][M // 2], d["z"][M // 2] = 0, 0
+    d["z"][0] = 0
+    got = zs.zs_block_join_backward(gy.to(dev), gh.to(dev), *on(d, dev), eps=1e-30)
+    ref = reference_grads(d, gy, gh, 1e-30)
+    close(got[0], ref[0], "grad_x", dtype, c)
+    close(got[1], ref[1], "grad_z", dtype, c)
+    for name, g, r in list(zip(NAMES, got, ref))[3:]:
+        close(g, r, "grad_" + name, F32, M * 4, floor=torch.full((1,), float(M) ** 0.5, dtype=torch.float64) * r.abs().max())
+    first = dict(x=d["x"], z=None, gate=None, scale=None, w_post=None, w_pre=d["w_pre"])
+    got = zs.zs_block_join_backward(None, gh.to(dev), *on(first, dev), eps=1e-30)
+    ref = reference_grads(first, None, gh, 1e-30)
+    close(got[0], ref[0], "grad_x of the norm", dtype, c)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate", [None, "row", "full"])
+@pytest.mark.parametrize("c, size", [(48, 1e-14), (48, 1e12), (48, 1e14), (48, 1e15), (520, 1e16), (1032, 1e16), (520, 1e17), (48, 1e18)])
+def test_rows_of_any_size(dev, dtype, gate, c, size):
+    """Rows far from 1: the gradient through the norm is a difference of terms of the size 1 / |y|, whatever powers of
+    |y| lie between.  Gradients of h alone (grad_y zeros, or none), since grad_y would hide theirs."""
+    M = 21
+    say("row size", c, dtype, gate, size)
+    d, _, gh = make(M, c, dtype, gate, seed=c)
+    d["x"] = (d["x"].float() * size).to(dtype)
+    if size < 1:
+        d["z"] = (d["z"].float() * size).to(dtype)
+    eps = 1e-30 if size < 1 else EPS
+    ref = reference_grads(d, None, gh, eps)
+    for gy in (torch.zeros(M, c, dtype=dtype), None):
+        got = zs.zs_block_join_backward(None if gy is None else gy.to(dev), gh.to(dev), *on(d, dev), eps=eps)
+        close(got[0], ref[0], "grad_x", dtype, c)
+        close(got[1], ref[1], "grad_z", dtype, c)
+        for name, g, r in list(zip(NAMES, got, ref))[3:]:
+            close(g, r, "grad_" + name, F32, M * 4, floor=torch.full((1,), float(M) ** 0.5, dtype=torch.float64) * r.abs().max())
