@@ -389,6 +389,9 @@ def block_norm(x: torch.Tensor, w_pre: torch.Tensor, eps: float = 1e-6) -> torch
 
 # ---- AdamW -------------------------------------------------------------------------------------------
 
+_dtype_of = torch.Tensor.dtype.__get__
+
+
 class AdamW:
     """AdamW over many fp32 parameter tensors, one kernel launch for up to 64
     of them.  Moments lie in one flat array each, tensor i from
@@ -447,6 +450,7 @@ class AdamW:
         self._shapes = [p.shape for p in self.params]
         self._words[3::6] = self._sizes = [p.numel() for p in self.params]
         self._words[4::6] = self.offsets
+        self._missing = False   # whether the table's sizes have zeros for missing gradients
 
     def _shape(self, name):
         return (self.total // STATE_BLOCK,) if name.endswith("_scale") else (self.total,)
@@ -483,22 +487,34 @@ class AdamW:
         _check("zs_adamw_step", status)
         s["step"] += 1
 
+    def _same(self, tensors, dtype) -> bool:
+        """Whether tensors still are what the constructor saw: a tensor's memory can
+        be replaced behind its back (``module.bfloat16()`` keeps the Parameter and
+        gives it another type's)."""
+        T = torch.Tensor
+        return (set(map(_dtype_of, tensors)) == {dtype}
+                and list(map(T.numel, tensors)) == self._sizes
+                and set(map(T.get_device, tensors)) == {self.device.index}
+                and all(map(T.is_contiguous, tensors)))
+
     def _fill(self, grads) -> None:
         """The table's addresses and types for this step.  All tensors are looked
         at in a few passes over the lists; what a pass finds is named one by one."""
         T, words, params, sizes = torch.Tensor, self._words, self.params, self._sizes
-        if any(g is None for g in grads):
+        missing = type(None) in set(map(type, grads))
+        if missing:
             # a tensor without a gradient gets a size of 0 and its own memory's address
             sizes = [0 if g is None else n for g, n in zip(grads, sizes)]
             grads = [p if g is None else g for g, p in zip(grads, params)]
-        index = {self.device.index}
-        types = [DTYPES.get(g.dtype) for g in grads]
+        types = list(map(DTYPES.get, map(_dtype_of, grads)))
         if (None in types or [g.shape for g in grads] != self._shapes
-                or [p.shape for p in params] != self._shapes
-                or set(map(T.get_device, grads)) != index or set(map(T.get_device, params)) != index
-                or not all(map(T.is_contiguous, grads)) or not all(map(T.is_contiguous, params))):
+                or set(map(T.get_device, grads)) != {self.device.index}
+                or not all(map(T.is_contiguous, grads)) or not self._same(params, torch.float32)
+                or self.copies is not None and not self._same(self.copies, torch.bfloat16)):
             for i, (g, shape) in enumerate(zip(grads, self._shapes)):
                 self._dense(params[i], f"params[{i}]", torch.float32, shape)
+                if self.copies is not None:
+                    self._dense(self.copies[i], f"copies[{i}]", torch.bfloat16, shape)
                 if g.dtype not in DTYPES:
                     raise TypeError(f"grads[{i}] must be float32 or bfloat16, got {g.dtype}")
                 self._dense(g, f"grads[{i}]", g.dtype, shape)
@@ -506,7 +522,9 @@ class AdamW:
         words[1::6] = list(map(T.data_ptr, grads))
         if self.copies is not None:
             words[2::6] = list(map(T.data_ptr, self.copies))
-        words[3::6] = sizes
+        if missing or self._missing:
+            words[3::6] = sizes
+        self._missing = missing
         words[5::6] = types
 
     def moments(self) -> tuple[torch.Tensor, torch.Tensor]:

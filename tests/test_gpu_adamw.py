@@ -290,3 +290,38 @@ def test_refusals(dev):
         setattr(o, name, value)
         with pytest.raises(zs.ZsError):
             o.step([torch.ones(4, device=dev)])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("which", ["params", "copies"])
+def test_memory_replaced_behind_the_optimizer(dev, bits, which):
+    """Parameters and copies whose memory was replaced by one of another type, size, device or layout after the
+    constructor looked at them are refused before any launch; one that fits is stepped."""
+    say("replaced memory", bits, which)
+
+    def make():
+        params = [torch.nn.Parameter(torch.ones(600, device=dev)) for _ in range(3)]
+        copies = [torch.zeros(600, dtype=BF16, device=dev) for _ in range(3)]
+        return params, copies, zs.AdamW(params, copies=copies, state_bits=bits, **HP)
+    kind = F32 if which == "params" else BF16
+    other = BF16 if which == "params" else F32
+    for bad, error in ((torch.zeros(600, dtype=other, device=dev), TypeError), (torch.zeros(300, dtype=kind, device=dev), ValueError),
+                       (torch.zeros(0, dtype=kind, device=dev), ValueError), (torch.zeros(600, dtype=kind), ValueError),
+                       (torch.zeros(1200, dtype=kind, device=dev)[::2], ValueError), (torch.zeros(600, dtype=torch.float64, device=dev), TypeError),
+                       (torch.zeros(600, dtype=torch.float16, device=dev), TypeError)):
+        params, copies, opt = make()
+        (params if which == "params" else copies)[1].data = bad
+        for grads in ([torch.ones(600, device=dev)] * 3, [torch.ones(600, device=dev), None, None]):
+            with pytest.raises(error):
+                opt.step(grads)
+        assert opt.state["step"] == 0 and (params[0] == 1).all() and (copies[0] == 0).all() and (opt.moments()[0] == 0).all()
+    module = torch.nn.Linear(20, 30, device=dev)   # as a model that is cast keeps its Parameters
+    opt = zs.AdamW(module.parameters(), state_bits=bits, **HP)
+    module.bfloat16()
+    module(torch.ones(2, 20, dtype=BF16, device=dev)).sum().backward()
+    with pytest.raises(TypeError):
+        opt.step()
+    params, copies, opt = make()
+    (params if which == "params" else copies)[1].data = torch.ones(600, dtype=kind, device=dev)
+    opt.step([torch.ones(600, device=dev)] * 3)
+    assert torch.equal(params[1], params[0]) and torch.equal(copies[1], copies[0]) and (params[1] != 1).all()
