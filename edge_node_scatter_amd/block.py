@@ -421,19 +421,13 @@ class AdamW:
             raise ValueError("copies must be one tensor for each parameter")
         self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
         self.state_bits = state_bits
-        self.offsets, total, ranges = [], 0, []
+        self.offsets, total = [], 0
         for i, p in enumerate(self.params):
             self._dense(p, f"params[{i}]", torch.float32, p.shape)
-            ranges.append((p.data_ptr(), p.data_ptr() + 4 * p.numel()))
             if self.copies is not None:
-                q = self.copies[i]
-                self._dense(q, f"copies[{i}]", torch.bfloat16, p.shape)
-                ranges.append((q.data_ptr(), q.data_ptr() + 2 * q.numel()))
+                self._dense(self.copies[i], f"copies[{i}]", torch.bfloat16, p.shape)
             self.offsets.append(total)
             total += -(-p.numel() // STATE_BLOCK) * STATE_BLOCK
-        ranges = sorted(r for r in ranges if r[0] < r[1])
-        if any(a[1] > b[0] for a, b in zip(ranges, ranges[1:])):
-            raise ValueError("parameters and copies must not share memory")
         self.total = total
         names = {32: ("m", "v"), 8: ("m_code", "m_scale", "v_code", "v_scale")}[state_bits]
         if state is None:
@@ -451,6 +445,7 @@ class AdamW:
         self._words[3::6] = self._sizes = [p.numel() for p in self.params]
         self._words[4::6] = self.offsets
         self._missing = False   # whether the table's sizes have zeros for missing gradients
+        self._apart(self._addresses())
 
     def _shape(self, name):
         return (self.total // STATE_BLOCK,) if name.endswith("_scale") else (self.total,)
@@ -497,6 +492,22 @@ class AdamW:
                 and set(map(T.get_device, tensors)) == {self.device.index}
                 and all(map(T.is_contiguous, tensors)))
 
+    def _addresses(self) -> list[int]:
+        """Of the parameters, then of the copies."""
+        T = torch.Tensor
+        at = list(map(T.data_ptr, self.params))
+        return at if self.copies is None else at + list(map(T.data_ptr, self.copies))
+
+    def _apart(self, at) -> None:
+        """Refuses parameters and copies at addresses where they share memory: one
+        launch writes them all, in no order."""
+        n = len(self.params)
+        ranges = sorted((a, a + (4 if i < n else 2) * self._sizes[i % n])
+                        for i, a in enumerate(at) if self._sizes[i % n])
+        if any(a[1] > b[0] for a, b in zip(ranges, ranges[1:])):
+            raise ValueError("parameters and copies must not share memory")
+        self._at = at
+
     def _fill(self, grads) -> None:
         """The table's addresses and types for this step.  All tensors are looked
         at in a few passes over the lists; what a pass finds is named one by one."""
@@ -518,10 +529,13 @@ class AdamW:
                 if g.dtype not in DTYPES:
                     raise TypeError(f"grads[{i}] must be float32 or bfloat16, got {g.dtype}")
                 self._dense(g, f"grads[{i}]", g.dtype, shape)
-        words[0::6] = list(map(T.data_ptr, params))
+        at, n = self._addresses(), len(params)
+        if at != self._at:
+            self._apart(at)
+        words[0::6] = at[:n]
         words[1::6] = list(map(T.data_ptr, grads))
         if self.copies is not None:
-            words[2::6] = list(map(T.data_ptr, self.copies))
+            words[2::6] = at[n:]
         if missing or self._missing:
             words[3::6] = sizes
         self._missing = missing

@@ -172,7 +172,7 @@ int zs_block_join_backward(const void *grad_y, const void *grad_h,
  * multiple of ZS_ADAMW_BLOCK, in increasing order and not in one another.
  * Elements between slices are not touched.  Parameters and copies of different
  * tensors must not share memory (not checked here: the host would compare all
- * pairs at every step; the binding's AdamW checks it once).
+ * pairs at every step; the binding's AdamW checks it where an address changed).
  */
 typedef struct zs_adamw_tensor {
     float *param;           /* [n], updated in place                          */

@@ -325,3 +325,30 @@ def test_memory_replaced_behind_the_optimizer(dev, bits, which):
     (params if which == "params" else copies)[1].data = torch.ones(600, dtype=kind, device=dev)
     opt.step([torch.ones(600, device=dev)] * 3)
     assert torch.equal(params[1], params[0]) and torch.equal(copies[1], copies[0]) and (params[1] != 1).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_memory_shared_after_construction(dev, bits):
+    """Parameters and copies that share memory since the constructor looked at them are refused; ones that merely moved
+    are stepped where they are now."""
+    say("shared memory", bits)
+    one = [torch.ones(600, device=dev)] * 3
+    for move in (lambda p, c: setattr(p[1], "data", p[0].data), lambda p, c: setattr(c[2], "data", c[0].data),
+                 lambda p, c: setattr(c[1], "data", p[1].data.view(BF16)[:600]),
+                 lambda p, c: setattr(p[2], "data", torch.cat([p[0].data, p[1].data])[:600]) or setattr(p[1], "data", p[2].data)):
+        params, copies = [torch.ones(600, device=dev) for _ in range(3)], [torch.zeros(600, dtype=BF16, device=dev) for _ in range(3)]
+        opt = zs.AdamW(params, copies=copies, state_bits=bits, **HP)
+        opt.step(one)
+        before = [t.clone() for t in (*params, *opt.moments())]
+        move(params, copies)
+        with pytest.raises(ValueError, match="share memory"):
+            opt.step(one)
+        with pytest.raises(ValueError, match="share memory"):
+            opt.step(one)
+        assert opt.state["step"] == 1 and torch.equal(params[0], before[0]) and torch.equal(opt.moments()[0], before[3])
+    params, copies = [torch.ones(600, device=dev) for _ in range(3)], [torch.zeros(600, dtype=BF16, device=dev) for _ in range(3)]
+    opt = zs.AdamW(params, copies=copies, state_bits=bits, **HP)
+    old = params[0].data
+    params[0].data, params[1].data = params[1].data, params[0].data.clone()
+    opt.step(one)
+    assert (old == 1).all() and torch.equal(params[0], params[2]) and torch.equal(params[1], params[2]) and (params[2] != 1).all()
