@@ -435,9 +435,9 @@ class AdamW:
                                                   device=self.device) for n in names}}
             if state_bits == 8:
                 state["seed"] = seed
-        for n in names:
-            self._dense(state[n], f"state[{n!r}]", self._dtype(n), self._shape(n))
+        self._arrays = [(n, self._dtype(n), torch.Size(self._shape(n))) for n in names]
         self.state = dict(state)
+        self._state()
         self._table = (_Tensor * len(self.params))()
         # the table as 64-bit words: param, grad, copy, n, state_offset, grad_dtype and reserved
         self._words = (ctypes.c_int64 * (6 * len(self.params))).from_buffer(self._table)
@@ -472,13 +472,13 @@ class AdamW:
         c = _Config(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
                     s["step"] + 1)
         lib = load_block()
+        at = self._state()
         if self.state_bits == 32:
-            status = _call(self.device, lib.zs_adamw_step, self._table, len(self._table), c,
-                           _ptr(s["m"]), _ptr(s["v"]), self.total)
+            status = _call(self.device, lib.zs_adamw_step, self._table, len(self._table), c, *at,
+                           self.total)
         else:
-            status = _call(self.device, lib.zs_adamw_step8, self._table, len(self._table), c,
-                           _ptr(s["m_code"]), _ptr(s["m_scale"]), _ptr(s["v_code"]),
-                           _ptr(s["v_scale"]), self.total, s["seed"] & 0xFFFFFFFF)
+            status = _call(self.device, lib.zs_adamw_step8, self._table, len(self._table), c, *at,
+                           self.total, s["seed"] & 0xFFFFFFFF)
         _check("zs_adamw_step", status)
         s["step"] += 1
 
@@ -492,6 +492,18 @@ class AdamW:
                 and set(map(T.get_device, tensors)) == {self.device.index}
                 and all(map(T.is_contiguous, tensors)))
 
+    def _state(self) -> list[int]:
+        """Addresses of the state arrays, in the calls' order, each looked at: the
+        dictionary is the caller's to change."""
+        at = []
+        for name, dtype, shape in self._arrays:
+            t = self.state[name]
+            if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape
+                    or t.get_device() != self.device.index or not t.is_contiguous()):
+                self._dense(t, f"state[{name!r}]", dtype, shape)
+            at.append(t.data_ptr())
+        return at
+
     def _addresses(self) -> list[int]:
         """Of the parameters, then of the copies."""
         T = torch.Tensor
@@ -499,13 +511,16 @@ class AdamW:
         return at if self.copies is None else at + list(map(T.data_ptr, self.copies))
 
     def _apart(self, at) -> None:
-        """Refuses parameters and copies at addresses where they share memory: one
-        launch writes them all, in no order."""
+        """Parameters and copies at these addresses from here on, unless they share
+        memory there: one launch writes them all, in no order."""
         n = len(self.params)
         ranges = sorted((a, a + (4 if i < n else 2) * self._sizes[i % n])
                         for i, a in enumerate(at) if self._sizes[i % n])
         if any(a[1] > b[0] for a, b in zip(ranges, ranges[1:])):
             raise ValueError("parameters and copies must not share memory")
+        self._words[0::6] = at[:n]
+        if self.copies is not None:
+            self._words[2::6] = at[n:]
         self._at = at
 
     def _fill(self, grads) -> None:
@@ -529,13 +544,10 @@ class AdamW:
                 if g.dtype not in DTYPES:
                     raise TypeError(f"grads[{i}] must be float32 or bfloat16, got {g.dtype}")
                 self._dense(g, f"grads[{i}]", g.dtype, shape)
-        at, n = self._addresses(), len(params)
+        at = self._addresses()
         if at != self._at:
             self._apart(at)
-        words[0::6] = at[:n]
         words[1::6] = list(map(T.data_ptr, grads))
-        if self.copies is not None:
-            words[2::6] = at[n:]
         if missing or self._missing:
             words[3::6] = sizes
         self._missing = missing
@@ -544,12 +556,11 @@ class AdamW:
     def moments(self) -> tuple[torch.Tensor, torch.Tensor]:
         """(m, v) flat in fp32: the state itself with 32 bits, the values that
         its codes stand for with 8."""
-        s = self.state
+        at = self._state()
         if self.state_bits == 32:
-            return s["m"], s["v"]
+            return self.state["m"], self.state["v"]
         m = torch.empty(self.total, dtype=torch.float32, device=self.device)
         v = torch.empty_like(m)
         _check("zs_adamw_moments8", _call(
-            self.device, load_block().zs_adamw_moments8, _ptr(s["m_code"]), _ptr(s["m_scale"]),
-            _ptr(s["v_code"]), _ptr(s["v_scale"]), self.total, _ptr(m), _ptr(v)))
+            self.device, load_block().zs_adamw_moments8, *at, self.total, _ptr(m), _ptr(v)))
         return m, v

@@ -352,3 +352,24 @@ def test_memory_shared_after_construction(dev, bits):
     params[0].data, params[1].data = params[1].data, params[0].data.clone()
     opt.step(one)
     assert (old == 1).all() and torch.equal(params[0], params[2]) and torch.equal(params[1], params[2]) and (params[2] != 1).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_state_replaced_behind_the_optimizer(dev, bits):
+    """State arrays put into the dictionary in place of the first ones: refused unless they have their type, size,
+    device and layout; those that do are the state from then on."""
+    say("replaced state", bits)
+    for name in ("m", "v") if bits == 32 else ("m_code", "m_scale", "v_code", "v_scale"):
+        p = torch.ones(600, device=dev)
+        opt = zs.AdamW([p], state_bits=bits, **HP)
+        old = opt.state[name]
+        for bad, error in ((old[:-1].clone(), ValueError), (old.cpu(), ValueError), (old.double(), TypeError), (old.repeat(2)[::2], ValueError), (None, ValueError),
+                           (old.view(1, -1), ValueError)):
+            opt.state[name] = bad
+            with pytest.raises(error):
+                opt.step([torch.ones(600, device=dev)])
+            with pytest.raises(error):
+                opt.moments()
+        opt.state[name] = old.clone()
+        opt.step([torch.ones(600, device=dev)])
+        assert opt.state["step"] == 1 and (p != 1).all() and (old == 0).all() and (opt.state[name] != 0).any()
