@@ -17,6 +17,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import HEADER_PATH, Csr, ZsError, _call, _check, _ptr, load
 
@@ -161,8 +162,8 @@ def zs_grouped_mm(x: torch.Tensor, w: torch.Tensor, groups: Csr,
     be a transposed view; ``out`` may have a row stride of at least n.  Rows of
     no group get zeros."""
     x, w = _mm_inputs(x, w, groups)
-    M, n = x.shape[0], w.shape[2]
-    if out is None:
+    M, n, given = x.shape[0], w.shape[2], out is not None
+    if not given:
         out = x.new_empty((M, n))
     else:
         _typed(out, "out", x.dtype, x.device)
@@ -170,6 +171,8 @@ def zs_grouped_mm(x: torch.Tensor, w: torch.Tensor, groups: Csr,
             raise ValueError(f"out must be ({M}, {n}) with contiguous rows")
     w, transposed = _weights(w)
     _check("zs_grouped_mm", _mm(x, w, transposed, groups, x.shape[1], n, out))
+    if given:
+        increment_version(out)
     return out
 
 
@@ -481,6 +484,11 @@ class AdamW:
                            self.total, s["seed"] & 0xFFFFFFFF)
         _check("zs_adamw_step", status)
         s["step"] += 1
+        # what the kernel wrote counts as changed in place, for graphs that saved it
+        written = self.params if self.copies is None else self.params + self.copies
+        if self._missing:
+            written = [t for t, g in zip(written, list(grads) * 2) if g is not None]
+        increment_version(written)
 
     def _same(self, tensors, dtype) -> bool:
         """Whether tensors still are what the constructor saw: a tensor's memory can

@@ -373,3 +373,23 @@ def test_state_replaced_behind_the_optimizer(dev, bits):
         opt.state[name] = old.clone()
         opt.step([torch.ones(600, device=dev)])
         assert opt.state["step"] == 1 and (p != 1).all() and (old == 0).all() and (opt.state[name] != 0).any()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_steps_count_as_changes(dev, bits):
+    """A step counts as a change of the parameters and copies it writes: a graph built before it refuses its backward,
+    as after any change in place.  A parameter without a gradient is not written and does not count."""
+    say("versions", bits)
+    p, q = (torch.randn(40, device=dev).requires_grad_() for _ in range(2))
+    copies = [torch.zeros(40, dtype=BF16, device=dev) for _ in range(2)]
+    opt = zs.AdamW([p, q], copies=copies, state_bits=bits, **HP)
+    loss = (p * p).sum()
+    other = (q * q).sum()
+    seen = [t._version for t in (p, q, *copies)]
+    opt.step([torch.ones(40, device=dev), None])
+    assert [t._version > v for t, v in zip((p, q, *copies), seen)] == [True, False, True, False]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    other.backward()
+    opt.step([torch.ones(40, device=dev), q.grad])
+    assert q._version > seen[1] and copies[1]._version > seen[3]

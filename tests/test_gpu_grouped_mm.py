@@ -351,3 +351,16 @@ def test_refusals(dev):
         zs.zs_grouped_mm(x, torch.zeros(2, 8, 8, device=dev), g, out=x)
     with pytest.raises(ValueError):
         zs.zs_grouped_mm_backward(torch.zeros(10, 5, device=dev), x, w, g)
+
+
+def test_output_counts_as_written(dev):
+    """Writing `out` counts as a change of it: a graph that saved its values refuses its backward."""
+    x, w = torch.ones(4, 8, device=dev), torch.ones(1, 8, 8, device=dev, requires_grad=True)
+    groups = groups_of(torch.tensor([0, 4], dtype=torch.int32), None, dev)
+    out = torch.ones(4, 8, device=dev)
+    before = out._version
+    loss = (out * zs.grouped_mm(x, w, groups)).sum()
+    zs.zs_grouped_mm(x, w.detach(), groups, out=out)
+    assert out._version > before
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
