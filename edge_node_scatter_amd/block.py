@@ -392,7 +392,7 @@ def block_norm(x: torch.Tensor, w_pre: torch.Tensor, eps: float = 1e-6) -> torch
 
 # ---- AdamW -------------------------------------------------------------------------------------------
 
-_dtype_of = torch.Tensor.dtype.__get__
+_dtype_of, _nbytes_of = torch.Tensor.dtype.__get__, torch.Tensor.nbytes.__get__
 
 
 class AdamW:
@@ -446,6 +446,7 @@ class AdamW:
         self._words = (ctypes.c_int64 * (6 * len(self.params))).from_buffer(self._table)
         self._shapes = [p.shape for p in self.params]
         self._words[3::6] = self._sizes = [p.numel() for p in self.params]
+        self._bytes = [4 * n for n in self._sizes], [2 * n for n in self._sizes]
         self._words[4::6] = self.offsets
         self._missing = False   # whether the table's sizes have zeros for missing gradients
         self._apart(self._addresses())
@@ -490,13 +491,13 @@ class AdamW:
             written = [t for t, g in zip(written, list(grads) * 2) if g is not None]
         increment_version(written)
 
-    def _same(self, tensors, dtype) -> bool:
-        """Whether tensors still are what the constructor saw: a tensor's memory can
-        be replaced behind its back (``module.bfloat16()`` keeps the Parameter and
-        gives it another type's)."""
+    def _same(self, tensors, sizes) -> bool:
+        """Whether tensors still have the bytes, device and layout that they had: a
+        tensor's memory can be replaced behind the optimizer (``module.bfloat16()``
+        keeps the Parameter and gives it another type's).  The type itself is looked
+        at where an address changed."""
         T = torch.Tensor
-        return (set(map(_dtype_of, tensors)) == {dtype}
-                and list(map(T.numel, tensors)) == self._sizes
+        return (list(map(_nbytes_of, tensors)) == sizes
                 and set(map(T.get_device, tensors)) == {self.device.index}
                 and all(map(T.is_contiguous, tensors)))
 
@@ -541,10 +542,11 @@ class AdamW:
             sizes = [0 if g is None else n for g, n in zip(grads, sizes)]
             grads = [p if g is None else g for g, p in zip(grads, params)]
         types = list(map(DTYPES.get, map(_dtype_of, grads)))
-        if (None in types or [g.shape for g in grads] != self._shapes
+        at = self._addresses()
+        if (None in types or at != self._at or [g.shape for g in grads] != self._shapes
                 or set(map(T.get_device, grads)) != {self.device.index}
-                or not all(map(T.is_contiguous, grads)) or not self._same(params, torch.float32)
-                or self.copies is not None and not self._same(self.copies, torch.bfloat16)):
+                or not all(map(T.is_contiguous, grads)) or not self._same(params, self._bytes[0])
+                or self.copies is not None and not self._same(self.copies, self._bytes[1])):
             for i, (g, shape) in enumerate(zip(grads, self._shapes)):
                 self._dense(params[i], f"params[{i}]", torch.float32, shape)
                 if self.copies is not None:
@@ -552,8 +554,6 @@ class AdamW:
                 if g.dtype not in DTYPES:
                     raise TypeError(f"grads[{i}] must be float32 or bfloat16, got {g.dtype}")
                 self._dense(g, f"grads[{i}]", g.dtype, shape)
-        at = self._addresses()
-        if at != self._at:
             self._apart(at)
         words[1::6] = list(map(T.data_ptr, grads))
         if missing or self._missing:
