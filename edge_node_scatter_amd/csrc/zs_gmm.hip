@@ -22,6 +22,7 @@
 #include <math.h>
 
 #include "zs_block_internal.h"
+#include "zs_launch.h"
 #include "zs_tile.h"
 
 namespace zs {
@@ -37,6 +38,7 @@ struct MmParams {
     const int32_t* perm;
     int64_t ldx, ldw, w_group, ldy, n_rows, n_groups;
     int k, n, n_tiles;
+    uint32_t first, grid;   // this launch's first workgroup, the workgroups of all launches
 };
 
 // WT: weights stored [n][k] (row form in LDS), else [k][n] (sum form).
@@ -65,8 +67,8 @@ __global__ __launch_bounds__(WM * WN * 64) void zs_gmm_kernel(const MmParams<T> 
         const int64_t o = p.offsets[v - 1];
         return o < 0 ? 0 : (o > p.n_rows ? p.n_rows : o);
     };
-    const TileOf tile = find_work(blockIdx.x, gridDim.x, p.n_tiles, false, p.n_groups + 2, BM, start,
-                                  [](int64_t) { return 0; });
+    const TileOf tile = find_work(p.first + blockIdx.x, p.grid, p.n_tiles, false, p.n_groups + 2, BM,
+                                  start, [](int64_t) { return 0; });
     if (tile.group < 0) return;
     const int n0 = __builtin_amdgcn_readfirstlane(tile.sub) * BN;
     const int group = __builtin_amdgcn_readfirstlane(tile.group) - 1;
@@ -242,10 +244,12 @@ hipError_t run(const GmmArgs& a, hipStream_t stream) {
     constexpr int BK = KB / sizeof(T);
     MmParams<T> p{static_cast<const T*>(a.x), static_cast<const T*>(a.w), static_cast<T*>(a.y),
                   a.offsets, a.perm, a.ldx, a.ldw, a.w_group, a.ldy, a.n_rows, a.n_groups,
-                  a.k, a.n, (a.n + BN - 1) / BN};
+                  a.k, a.n, (a.n + BN - 1) / BN, 0, 0};
     const int64_t slots = a.n_rows / BM + a.n_groups + 2;
     const int64_t grid = work_grid(slots, p.n_tiles, false);
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;   // operands far above 288 GB
+    // at most 2^29 for the groups; more for rows only with outputs above 288 GB
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    p.grid = uint32_t(grid);
     // no more buffers than stages: short sums leave LDS for more workgroups
     const int stages = (a.k + BK - 1) / BK;
     const int bytes = (stages < S ? stages : S) * (BM + pow2_at_least(BN)) * KB;
@@ -255,8 +259,11 @@ hipError_t run(const GmmArgs& a, hipStream_t stream) {
             reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (err != hipSuccess) return err;
     }
-    kernel<<<dim3(unsigned(grid)), WM * WN * 64, bytes, stream>>>(p);
-    return hipGetLastError();
+    return launch_ranges(grid, WM * WN * 64, [&](int64_t first, int64_t count) {
+        p.first = uint32_t(first);
+        kernel<<<dim3(unsigned(count)), WM * WN * 64, bytes, stream>>>(p);
+        return hipGetLastError();
+    });
 }
 
 template <typename T, bool WT>

@@ -23,6 +23,7 @@
 //  - 16384 rows, one group, 4096 x 4096, bf16: 680 us, 810 TFLOP/s; two transposed
 //    LDS reads feed each matrix instruction's operand.
 #include "zs_block_internal.h"
+#include "zs_launch.h"
 #include "zs_tile.h"
 
 namespace zs {
@@ -44,6 +45,7 @@ struct WgParams {
     T* gx;
     int64_t ldw, w_group;
     bool spread;   // each XCD takes an eighth of every piece's tiles
+    uint32_t first, grid;   // this launch's first workgroup, the workgroups of all launches
 };
 
 __device__ inline int64_t clamp_offset(const int32_t* offsets, int64_t v, int64_t n_rows) {
@@ -81,7 +83,7 @@ __global__ __launch_bounds__(WA * WN * 64) void zs_wgrad_kernel(const WgParams<T
         return clamp_offset(p.offsets, BOTH ? v - 1 : v, p.n_rows);
     };
     const auto least = [&](int64_t v) { return BOTH && (v == 0 || v == p.n_groups + 1) ? 0 : 1; };
-    const TileOf tile = find_work(blockIdx.x, gridDim.x, p.k_tiles * p.n_tiles, p.spread,
+    const TileOf tile = find_work(p.first + blockIdx.x, p.grid, p.k_tiles * p.n_tiles, p.spread,
                                   p.n_groups + (BOTH ? 2 : 0), p.piece, start, least);
     if (tile.group < 0) return;
     const int in_slot = __builtin_amdgcn_readfirstlane(tile.sub);
@@ -351,7 +353,8 @@ hipError_t run(WgParams<T> p, hipStream_t stream) {
     p.spread = p.k_tiles * p.n_tiles >= 16 && p.n_groups <= kCountedGroups;
     const int64_t slots = p.n_rows / p.piece + p.n_groups + (BOTH ? 2 : 0);
     const int64_t grid = work_grid(slots, int64_t(p.k_tiles) * p.n_tiles, p.spread);
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;   // operands far above 288 GB
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;   // gradients above 288 GB
+    p.grid = uint32_t(grid);
     const int64_t longest = p.piece < p.n_rows ? p.piece : p.n_rows;
     const int stages = int((longest + BR - 1) / BR);
     const int bytes = (stages < 1 ? 1 : stages < S ? stages : S) * (BA + pow2_at_least(BN)) * KB;
@@ -361,8 +364,11 @@ hipError_t run(WgParams<T> p, hipStream_t stream) {
             reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (err != hipSuccess) return err;
     }
-    kernel<<<dim3(unsigned(grid)), 256, bytes, stream>>>(p);
-    return hipGetLastError();
+    return launch_ranges(grid, 256, [&](int64_t first, int64_t count) {
+        p.first = uint32_t(first);
+        kernel<<<dim3(unsigned(count)), 256, bytes, stream>>>(p);
+        return hipGetLastError();
+    });
 }
 
 template <typename T, int BA, bool BOTH>
@@ -388,7 +394,7 @@ hipError_t dispatch(const WgradArgs& a, hipStream_t stream) {
     WgParams<T> p{static_cast<const T*>(a.x), static_cast<const T*>(a.gy), static_cast<T*>(a.gw),
                   a.partial, a.offsets, a.perm, a.ldx, a.ldg, a.n_rows, a.n_groups, a.piece,
                   a.k, a.n, 0, 0, static_cast<const T*>(a.w), static_cast<T*>(a.gx), a.ldw,
-                  a.w_group, false};
+                  a.w_group, false, 0, 0};
     const bool vec = vectors(a, sizeof(T) == 2);
     hipError_t err;
     const int side = tile_side(a.k, false);

@@ -185,3 +185,35 @@ def test_kernels_keep_their_values_in_registers(tmp_path):
             assert m.group(1) == "0", path
         assert not re.search(r"\.private_segment_fixed_size:\s+[1-9]", text), path
     assert seen > 20
+
+
+def test_launches_of_large_grids(tmp_path):
+    """launch_ranges: every workgroup once, in order, fewer than 2^32 threads a launch, starts on multiples of 8, and no
+    launch after an error."""
+    src = tmp_path / "t.cpp"
+    src.write_text("""
+#include <cstdlib>
+#include <initializer_list>
+#include "zs_launch.h"
+int main() {
+    for (int threads : {256, 512, 1024})
+        for (int64_t grid : {int64_t(1), (int64_t(1) << 23) - 1, int64_t(1) << 23, (int64_t(1) << 24) - 8, int64_t(1) << 24, (int64_t(1) << 24) + 25, int64_t(0x7fffffff)}) {
+            int64_t at = 0;
+            int calls = 0;
+            const int err = zs::launch_ranges(grid, threads, [&](int64_t first, int64_t count) {
+                if (first != at || first % 8 || count < 1 || count * threads >= int64_t(1) << 32) std::abort();
+                at += count;
+                ++calls;
+                return 0;
+            });
+            if (err || at != grid || (grid * threads < (int64_t(1) << 32) - 8 * threads && calls != 1)) std::abort();
+        }
+    int calls = 0;
+    if (zs::launch_ranges(int64_t(1) << 30, 256, [&](int64_t, int64_t) { return ++calls == 3 ? 7 : 0; }) != 7 || calls != 3) std::abort();
+    if (zs::launch_ranges(0, 256, [&](int64_t, int64_t) { return 9; })) std::abort();
+    return 0;
+}
+""")
+    exe = tmp_path / "t"
+    subprocess.check_call(["g++", "-std=c++17", "-Wall", "-Werror", "-I", zs_build.CSRC, str(src), "-o", str(exe)])
+    assert subprocess.call([str(exe)]) == 0

@@ -364,3 +364,43 @@ def test_output_counts_as_written(dev):
     assert out._version > before
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_more_workgroups_than_one_launch_holds(dev, dtype):
+    """A launch has less than 2^32 threads.  The most groups, few of them with rows, and columns enough for 2^24
+    workgroups: windows of one array as the groups' weights (each group its own), and a weight gradient of 2 or 4 GiB."""
+    M, G, k, n = 1000, 1 << 20, 8, 2048
+    say("many workgroups", dtype)
+    rng = np.random.default_rng(7)
+    gen = torch.Generator().manual_seed(7)
+    at = np.sort(np.concatenate([rng.integers(0, M + 1, G - 1), [0, M]]))
+    at[:G // 3] = 0   # the first rows belong to a group far behind
+    off = torch.from_numpy(at.astype(np.int32))
+    p = torch.from_numpy(rng.permutation(M).astype(np.int32))
+    groups = groups_of(off, p, dev)
+    x = torch.randint(-2, 3, (M, k), generator=gen).to(dtype)
+    base = torch.randint(-2, 3, (G * 8 + k * n,), generator=gen).to(dtype).to(dev)
+    y = zs.zs_grouped_mm(x.to(dev), base.as_strided((G, k, n), (8, n, 1)), groups).cpu()
+    pos = torch.searchsorted(off[1:].long(), torch.arange(M), right=True)
+    base = base.cpu()
+    for i in range(M):
+        r, g = int(p[i]), int(pos[i])
+        want = x[r].double() @ base.as_strided((k, n), (n, 1), g * 8).double()
+        assert torch.equal(y[r], want.to(dtype)), (i, g)
+    del base, y
+    k, n = 1, 1024
+    x, gy = (torch.randint(-2, 3, s, generator=gen).to(dtype) for s in ((M, k), (M, n)))
+    stale = torch.full((G, k, n), 7.0, dtype=dtype, device=dev)   # the memory the gradient then gets
+    w = torch.ones(1, k, n, dtype=dtype, device=dev).expand(G, k, n)
+    del stale
+    gx, gw = zs.zs_grouped_mm_backward(gy.to(dev), x.to(dev), w, groups)
+    assert torch.equal(gx.cpu(), gy.double().sum(1, keepdim=True).to(dtype))
+    live = torch.unique(pos)
+    want = torch.zeros(len(live), k, n, dtype=torch.float64)
+    for j, g in enumerate(live.tolist()):
+        r = blockref.group_rows(off, p, g)
+        want[j] = x[r].double().T @ gy[r].double()
+    assert torch.equal(gw[live.to(dev)].cpu(), want.to(dtype))
+    gw[live.to(dev)] = 0
+    assert gw.count_nonzero().item() == 0
