@@ -133,7 +133,8 @@ def _mm(x, w, transposed, groups, k, n, out):
     row = w.stride(2) if transposed else w.stride(1)
     return _call(x.device, load_block().zs_grouped_mm, _ptr(x), x.stride(0), _ptr(w), w.stride(0),
                  row, transposed, _ptr(groups.rowptr), _ptr(groups.perm), x.shape[0],
-                 groups.n_nodes, k, n, DTYPES[x.dtype], _ptr(out), out.stride(0))
+                 groups.n_nodes, k, n, DTYPES[x.dtype], _ptr(out),
+                 out.stride(0) if x.shape[0] > 1 else n)   # a single row's stride says nothing
 
 
 def _mm_inputs(x, w, groups):

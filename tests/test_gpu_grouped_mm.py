@@ -404,3 +404,13 @@ def test_more_workgroups_than_one_launch_holds(dev, dtype):
     assert torch.equal(gw[live.to(dev)].cpu(), want.to(dtype))
     gw[live.to(dev)] = 0
     assert gw.count_nonzero().item() == 0
+
+
+def test_output_of_one_row(dev):
+    """The stride of a single row's dimension says nothing: a column's transpose is such an output."""
+    x, w = torch.ones(1, 8, device=dev), torch.ones(2, 8, 24, device=dev)
+    groups = groups_of(torch.tensor([0, 1, 1], dtype=torch.int32), None, dev)
+    out = torch.zeros(24, 1, device=dev).t()
+    assert out.stride(0) < 24
+    zs.zs_grouped_mm(x, w, groups, out=out)
+    assert (out == 8).all()
