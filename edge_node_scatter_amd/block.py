@@ -315,8 +315,9 @@ def zs_block_join(x: torch.Tensor, z: torch.Tensor | None, gate: torch.Tensor | 
     x, z and gate are float32 or bfloat16 and may have a row stride; gate is
     (M, c), (M, 1) or None; scale, w_post and w_pre are float32 (c,).  h is None
     when w_pre is; without z, y is x itself and h its norm."""
+    given = x
     x, z, gate, scale, w_post, w_pre = _join_inputs(x, z, gate, scale, w_post, w_pre)
-    y = x if z is None else x.new_empty(x.shape)
+    y = given if z is None else x.new_empty(x.shape)
     h = None if w_pre is None else x.new_empty(x.shape)
     _check("zs_block_join", _call(
         x.device, load_block().zs_block_join, *_join_args(x, z, gate, scale, w_post, w_pre, eps),

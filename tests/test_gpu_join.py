@@ -365,3 +365,10 @@ def test_rows_of_any_size(dev, dtype, gate, c, size):
         close(got[1], ref[1], "grad_z", dtype, c)
         for name, g, r in list(zip(NAMES, got, ref))[3:]:
             close(g, r, "grad_" + name, F32, M * 4, floor=torch.full((1,), float(M) ** 0.5, dtype=torch.float64) * r.abs().max())
+
+
+def test_without_a_block_y_is_x(dev):
+    x, w = torch.randn(6, 16, device=dev), torch.ones(16, device=dev)
+    for t in (x, x.t().contiguous().t(), torch.randn(6, 20, device=dev)[:, :16]):
+        y, h = zs.zs_block_join(t, None, None, None, None, w, eps=EPS)
+        assert y is t and h.shape == t.shape
