@@ -414,3 +414,35 @@ def test_output_of_one_row(dev):
     assert out.stride(0) < 24
     zs.zs_grouped_mm(x, w, groups, out=out)
     assert (out == 8).all()
+
+
+def whole(M, G, k, n, dtype, perm, seed, empty=True):
+    """make() with whole numbers of at most 2: every sum below 2^24 is exact in fp32, so results are the definition's
+    rounded once and have to be equal to it."""
+    _, _, _, off, p = make(M, G, 1, 1, dtype, perm, seed, empty)
+    gen = torch.Generator().manual_seed(seed)
+    assert 4 * max(M, k, n) < 1 << 24
+    mk = lambda *s: torch.randint(-2, 3, s, generator=gen).to(dtype)  # noqa: E731
+    return mk(M, k), mk(G, k, n), mk(M, n), off, p
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(5000, 3, 32, 96), (20000, 2, 24, 40), (9000, 40, 64, 64), (9000, 3, 776, 1160), (9000, 3, 777, 1161), (900000, 2, 32, 96)])
+@pytest.mark.parametrize("perm", [False, True])
+def test_cut_groups_exactly(dev, dtype, shape, perm):
+    """Both gradients where groups are cut into pieces: pieces longer than the 1024 row indices that a workgroup holds
+    at a time (the last three; 1230 rows and 1172), wide weights whose tiles are spread over the XCDs, operands off 16
+    bytes, and the one pass of narrow weights."""
+    M, G, k, n = shape
+    say("cut groups", shape, dtype, "perm" if perm else "sorted")
+    x, w, gy, off, p = whole(M, G, k, n, dtype, perm, seed=k)
+    groups = groups_of(off, p, dev)
+    gx, gw = zs.zs_grouped_mm_backward(gy.to(dev), x.to(dev), w.to(dev), groups)
+    alone = zs.zs_grouped_mm_backward(gy.to(dev), x.to(dev), w.to(dev), groups, need_x=False)[1]
+    for g in range(G):
+        r = blockref.group_rows(off, p, g)
+        a, b = x[r].double(), gy[r].double()
+        want = (a.T @ b).to(dtype)
+        assert torch.equal(gw[g].cpu(), want), f"grad_w of group {g}"
+        assert torch.equal(alone[g].cpu(), want), f"grad_w of group {g}, alone"
+        assert torch.equal(gx[r.to(dev)].cpu(), (b @ w[g].double().T).to(dtype)), f"grad_x of group {g}"
