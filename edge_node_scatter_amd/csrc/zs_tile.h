@@ -44,8 +44,10 @@ __device__ inline uint32_t lds_offset(const void* p) {
 // over the wavefront), past the registers.  Completion is counted in vmcnt;
 // wait_loads() before the barrier that publishes the tile.  Inline assembly
 // because the compiler otherwise drains all such loads before every transposed
-// LDS read, whichever buffer it reads.  The instruction has no output registers,
-// and m0 is otherwise unused here (gfx9 LDS accesses do not read it).
+// LDS read, whichever buffer it reads.  The instruction has no output registers.
+// m0 is reserved, so a clobber list cannot name it: no kernel with these loads may
+// have another use of m0 (gfx9 LDS accesses do not read it), which a test of the
+// listings holds.
 __device__ inline void load_to_lds(const void* g, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                  :

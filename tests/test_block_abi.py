@@ -217,3 +217,24 @@ int main() {
     exe = tmp_path / "t"
     subprocess.check_call(["g++", "-std=c++17", "-Wall", "-Werror", "-I", zs_build.CSRC, str(src), "-o", str(exe)])
     assert subprocess.call([str(exe)]) == 0
+
+
+def test_m0_belongs_to_the_loads_to_lds(tmp_path):
+    """Inline assembly writes m0 without being able to say so: in kernels with those loads every mention of m0 is its
+    write right before a load, and no instruction reads it unnamed."""
+    loads = 0
+    for path in zs_build.device_asm(str(tmp_path)):
+        if not os.path.basename(path).startswith(("zs_gmm", "zs_wgrad")):
+            continue
+        for body in re.findall(r"^_Z\S+:[^\n]*\n(.*?)^\.Lfunc_end", open(path).read(), flags=re.M | re.S):
+            lines = [x.split(";")[0].strip() for x in body.splitlines()]
+            lines = [x for x in lines if x and not x.startswith(".")]
+            if not any("load_lds" in x for x in lines):
+                continue
+            for i, x in enumerate(lines):
+                if re.search(r"\bm0\b", x):
+                    assert x.startswith("s_mov_b32 m0, s") and lines[i + 1] == "s_nop 0" and lines[i + 2].startswith("global_load_lds_dwordx4"), x
+                    loads += 1
+                assert not re.match(r"(s_movrel|v_movrel|s_set_gpr_idx|s_sendmsg|v_interp|ds_gws|ds_append|ds_consume|ds_ordered|buffer_load\S* .*\blds\b)", x), x
+            assert sum(bool(re.search(r"\bm0\b", x)) for x in lines) == sum(x.startswith("global_load_lds") for x in lines)
+    assert loads > 100
