@@ -410,6 +410,11 @@ class AdamW:
     ``copies``: bf16 tensors that receive each new parameter rounded (the
     working copies that bf16 products read), or None.  ``state``: an earlier
     ``AdamW.state``, taken over in place.
+
+    Rate and decay are one for all of an object's tensors: tensors that shall
+    not decay take an object of their own.  A step captured in a HIP graph is
+    counted once, at the capture, and every replay is that step again (the same
+    bias corrections and random bits): capture what leads up to it instead.
     """
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,

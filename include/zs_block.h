@@ -13,7 +13,8 @@
  *  - Strides are in elements, the last dimension is contiguous, and a view
  *    spans at most 2^60 elements.
  *  - No call allocates, synchronises or records a memset, so all of them can
- *    be captured in a HIP graph.
+ *    be captured in a HIP graph.  A captured AdamW step is not the next step
+ *    at each replay but its own again (see zs_adamw_step).
  *  - Results are run-to-run deterministic (no atomics).
  */
 #ifndef ZS_BLOCK_H_
@@ -173,6 +174,12 @@ int zs_block_join_backward(const void *grad_y, const void *grad_h,
  * Elements between slices are not touched.  Parameters and copies of different
  * tensors must not share memory (not checked here: the host would compare all
  * pairs at every step; the binding's AdamW checks it where an address changed).
+ *
+ * The config is a host struct too, so a call captured in a HIP graph holds its
+ * step: every replay applies that number's bias corrections and rate and, in
+ * zs_adamw_step8, adds the same random bits to the same elements, so that a
+ * moment which these bits never carry over stays on its code.  A training loop
+ * captures its products and gradients and calls the step itself.
  */
 typedef struct zs_adamw_tensor {
     float *param;           /* [n], updated in place                          */
