@@ -10,13 +10,13 @@
 // PFLOP/s in bf16 and 150 TFLOP/s in fp32):
 //  - 158002 rows, 8 uneven groups of 9, 32 -> 96, fp32, perm: 23 us, 3.5 TB/s.  Bound
 //    by memory (16 us); the workgroups, few for each compute unit, load, multiply
-//    (matrix cores 33 % busy) and store largely in step.  Rows streamed past weights
+//    (matrix cores 30 % busy) and store largely in step.  Rows streamed past weights
 //    held in registers, without LDS, took 28 us.
-//  - 16384 rows, 7 uneven groups of 8, 1024 -> 2048, bf16: 94 us, 730 TFLOP/s; one
-//    group, 4096 -> 4096: 531 us, 1035 TFLOP/s (1110 with weights [n][k]).  A
-//    256 x 256 stage is 2048 cycles of matrix instructions and as many of loads to
-//    LDS (a wavefront's 1 KB takes the address unit 32 cycles), and their overlap is
-//    not complete: matrix cores busy 55 % of the time.
+//  - 16384 rows, 7 uneven groups of 8, 1024 -> 2048, bf16: 85 us, 808 TFLOP/s (matrix
+//    cores busy 42 % of the time); one group, 4096 -> 4096: 488 us, 1127 TFLOP/s (1157
+//    with weights [n][k]).  A 256 x 256 stage is 2048 cycles of matrix instructions
+//    and as many of loads to LDS (a wavefront's 1 KB takes the address unit 32
+//    cycles), and their overlap is not complete: matrix cores busy 53 % of the time.
 //  - 96 rows, 4 groups, 64 -> 64, fp32: 4.8 us, of which most is latency: offsets,
 //    row indices and operands are read one after the other.
 #include <math.h>
@@ -286,8 +286,8 @@ hipError_t dispatch(const GmmArgs& a, hipStream_t stream) {
         // compute unit; of 256 rows, or of 192 where their last round of workgroups
         // leaves less idle (a group has half a tile of padding on average; of many
         // rounds the last is less than a whole one, as workgroups drift apart).
-        // 16384 x 1024 -> 2048 in 7 uneven groups: 95 us with 192 rows, 108 with 256;
-        // 16384 x 4096 -> 4096 in one group: 596 us with 192, 543 with 256.
+        // 16384 x 1024 -> 2048 in 7 uneven groups: 84 us with 192 rows, 95 with 256;
+        // 16384 x 4096 -> 4096 in one group: 551 us with 192, 489 with 256.
         if constexpr (sizeof(T) == 2) {
             if (tiles(256, 256) >= 256) {
                 const auto cost = [&](int bm) {

@@ -19,10 +19,10 @@
 // sums are added in order by a second kernel.
 //
 // Bound by memory.  Measured on MI355X (a copy reaches 5.1 TB/s):
-//  - gradients of 32768 x 2048 in bf16: 236 us and 5 us for the partial sums, 4.5 TB/s
+//  - gradients of 32768 x 2048 in bf16: 241 us and 5 us for the partial sums, 4.5 TB/s
 //    of 1.07 GB; some 60 vector instructions an element beside them (a workgroup a
 //    row, a chunk a lane, the next row's loads in flight; without those 363 us).
-//  - gradients of 16384 x 520 in fp32: 42 and 4 us, 4.9 TB/s of 205 MB (130 chunks of
+//  - gradients of 16384 x 520 in fp32: 44 and 4 us, 4.7 TB/s of 205 MB (130 chunks of
 //    a wavefront's 192).
 //  - forward of 65536 x 32 in fp32: 9.7 us, 4.3 TB/s of 42 MB.
 #include "zs_block_internal.h"

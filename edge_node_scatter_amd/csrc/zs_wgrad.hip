@@ -17,10 +17,11 @@
 //    (81 us at a copy's rate); the weight gradient alone 66 us, at a copy's rate.
 //    The fp32 matrix instructions (48 a wavefront and stage) are 50 us of it and
 //    overlap the loads only in part.
-//  - 8191 rows, 14 uneven groups of 16, 776 x 1160, bf16: 46 us and 7 us for the
-//    partial sums.  Bound by the start and end of its short work items (7 stages on
-//    average, two and a half rounds of them) and by what the longest group leaves.
-//  - 16384 rows, one group, 4096 x 4096, bf16: 680 us, 810 TFLOP/s; two transposed
+//  - 8191 rows, 14 uneven groups of 16, 776 x 1160, bf16: 48 us and 7 us for the
+//    partial sums, matrix cores busy 22 % of the time.  Bound by the start and end of
+//    its short work items (7 stages on average, two and a half rounds of them) and by
+//    what the longest group leaves.
+//  - 16384 rows, one group, 4096 x 4096, bf16: 635 us, 865 TFLOP/s; two transposed
 //    LDS reads feed each matrix instruction's operand.
 #include "zs_block_internal.h"
 #include "zs_launch.h"

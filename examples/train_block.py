@@ -7,6 +7,10 @@ features (grouped_mm over zs_build_csr of the pair index), the scatter sums them
 follows on the rows of the padded node layout: a norm, products with weights and a gate by the node's species, and
 the gated join with the norm behind it.  A linear readout is fitted to the values of a teacher of the same form.
 All parameters are stepped by AdamW.  The data are synthetic.
+
+It shows the calls together, not a potential: a norm and a gate of each padded row by itself do not keep how the rows
+of one degree turn into each other under rotation.  Norm weights are kept as their distance from 1, so that the decay
+that all tensors share draws them to 1.
 """
 from __future__ import annotations
 
