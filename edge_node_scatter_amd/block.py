@@ -571,9 +571,9 @@ class AdamW:
     def moments(self) -> tuple[torch.Tensor, torch.Tensor]:
         """(m, v) flat in fp32: the state itself with 32 bits, the values that
         its codes stand for with 8."""
-        at = self._state()
-        if self.state_bits == 32:
+        if self.state_bits == 32:   # the caller's own arrays: nothing reads them here
             return self.state["m"], self.state["v"]
+        at = self._state()
         m = torch.empty(self.total, dtype=torch.float32, device=self.device)
         v = torch.empty_like(m)
         _check("zs_adamw_moments8", _call(
