@@ -26,7 +26,9 @@ page ("What", third bullet), with the envelope gradient it carries.
 
 ``edge_node_scatter_amd.block`` binds the learned operators around the scatter
 (``grouped_mm``, ``block_join``, ``block_norm``, ``AdamW`` and the functions
-under them); they are imported here too.
+under them), ``edge_node_scatter_amd.layers`` those before, between and behind a
+block's products (``embedding``, ``layer_norm``, ``route``, ``combine``); they are
+imported here too.
 """
 from __future__ import annotations
 
@@ -456,3 +458,6 @@ def gie_zonal_scatter_normalized(coupling: torch.Tensor, radial: torch.Tensor, e
 
 from .block import (AdamW, block_join, block_norm, grouped_mm, sorted_groups,  # noqa: E402, F401
                     zs_block_join, zs_block_join_backward, zs_grouped_mm, zs_grouped_mm_backward)
+from .layers import (Router, combine, embedding, expert_groups, layer_norm, route,  # noqa: E402, F401
+                     zs_combine, zs_combine_backward, zs_embedding, zs_embedding_backward,
+                     zs_layer_norm, zs_layer_norm_backward, zs_route, zs_route_backward)

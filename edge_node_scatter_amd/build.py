@@ -24,7 +24,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libzs.so")
 SOURCES = ["zs_api.hip", "zs_csr.hip", "zs_fwd.hip", "zs_bwd.hip", "zs_norm.hip",
-           "zs_block_api.hip", "zs_gmm.hip", "zs_wgrad.hip", "zs_join.hip", "zs_adamw.hip"]
+           "zs_block_api.hip", "zs_gmm.hip", "zs_wgrad.hip", "zs_join.hip", "zs_adamw.hip",
+           "zs_layers_api.hip", "zs_embed.hip", "zs_lnorm.hip", "zs_route.hip", "zs_combine.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -37,7 +38,7 @@ FLAGS = [
 ]
 
 
-JOBS = 4   # sources compiled at a time
+JOBS = 8   # sources compiled at a time
 
 
 def _run(cmd: list[str], verbose: bool = False) -> None:

@@ -1,0 +1,200 @@
+// Weighted sum of the experts' rows of a token and its gradients, gfx950.
+//
+//   y[t] = sum_j w[t][j] z[t k + j];  dz[t k + j] = w[t][j] dy[t],
+//   dw[t][j] = <dy[t], z[t k + j]>
+//
+// Bound by memory: every row of z is read once.  Forward: a lane holds a chunk of y
+// and takes its slots four loads at a time.  Backward: the L lanes of a token hold
+// dy[t], so that it is read once too, and the k dot products cross the lanes (and,
+// above a wavefront, LDS).
+#include "zs_launch.h"
+#include "zs_layers_internal.h"
+#include "zs_row.h"
+
+namespace zs {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T>
+struct CombineParams {
+    const T* z;
+    const float* weight;
+    int64_t ldz, n_rows, block0;
+    int k, c, blocks;   // column blocks of L chunks
+    bool vec;
+    T* y;
+    const T* gy;
+    int64_t ldg;
+    T* gz;
+    float* gw;
+};
+
+template <typename T, int L>
+__global__ __launch_bounds__(kThreads) void zs_combine_kernel(const CombineParams<T> p) {
+    constexpr int V = Chunk<T>::V, kRows = kThreads / L, kLoads = 4;
+    const int64_t block = p.block0 + blockIdx.x;
+    const int l = threadIdx.x % L, slot = threadIdx.x / L;
+    const int64_t t = block / p.blocks * kRows + slot;
+    const int chunk = int(block % p.blocks) * L + l;
+    if (t >= p.n_rows || chunk * V >= p.c) return;
+    const T* z = p.z + t * p.k * p.ldz;
+    const float* w = p.weight + t * p.k;
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    int j = 0;
+    for (; j + kLoads <= p.k; j += kLoads) {
+        u32x4 raw[kLoads];
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q)
+            raw[q] = load_chunk(z + (j + q) * p.ldz, chunk, p.c, p.vec);
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) {
+            float f[V];
+            Chunk<T>::unpack(raw[q], f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w[j + q], f[i], acc[i]);
+        }
+    }
+    for (; j < p.k; ++j) {
+        float f[V];
+        Chunk<T>::unpack(load_chunk(z + j * p.ldz, chunk, p.c, p.vec), f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w[j], f[i], acc[i]);
+    }
+    store_any(p.y + t * p.c, chunk, p.c, p.vec, Chunk<T>::pack(acc));
+}
+
+constexpr int threads_of(int L) { return L > kThreads ? L : kThreads; }
+
+template <typename T, int L, int NV>
+__global__ __launch_bounds__(threads_of(L)) void zs_combine_bwd_kernel(const CombineParams<T> p) {
+    constexpr int V = Chunk<T>::V, kRows = threads_of(L) / L, kWaves = L > 64 ? L / 64 : 1;
+    __shared__ float dots[kWaves > 1 ? kWaves * ZS_MAX_SLOTS : 1];
+    const int l = threadIdx.x % L, slot = threadIdx.x / L;
+    for (int64_t base = int64_t(blockIdx.x) * kRows; base < p.n_rows;
+         base += int64_t(gridDim.x) * kRows) {
+        const int64_t t = base + slot;
+        const bool live = t < p.n_rows;
+        const int c = live ? p.c : 0;
+        float g[NV][V];
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+            Chunk<T>::unpack(load_chunk(p.gy + t * p.ldg, l + n * L, c, p.vec), g[n]);
+        if constexpr (kWaves > 1) __syncthreads();   // the last token's dots are read
+        for (int j = 0; j < p.k; ++j) {
+            const int64_t row = t * p.k + j;
+            const float w = live ? p.weight[row] : 0.0f;
+            u32x4 raw[NV];
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+                raw[n] = load_chunk(p.z + row * p.ldz, l + n * L, c, p.vec);
+            float dot = 0.0f;
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                float z[V];
+                Chunk<T>::unpack(raw[n], z);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    dot = __builtin_fmaf(g[n][i], z[i], dot);
+                    z[i] = w * g[n][i];
+                }
+                if (live) store_any(p.gz + row * p.c, l + n * L, c, p.vec, Chunk<T>::pack(z));
+            }
+            dot = lane_sum<(L < 64 ? L : 64)>(dot);
+            if constexpr (kWaves > 1) {
+                if ((threadIdx.x & 63) == 0) dots[(threadIdx.x >> 6) * ZS_MAX_SLOTS + j] = dot;
+            } else if (l == 0 && live) {
+                p.gw[row] = dot;
+            }
+        }
+        if constexpr (kWaves > 1) {
+            __syncthreads();
+            if (int(threadIdx.x) < p.k) {
+                float s = 0.0f;
+#pragma unroll
+                for (int v = 0; v < kWaves; ++v) s += dots[v * ZS_MAX_SLOTS + threadIdx.x];
+                p.gw[t * p.k + threadIdx.x] = s;
+            }
+        }
+    }
+}
+
+template <typename T>
+CombineParams<T> params(const CombineArgs& a) {
+    constexpr int V = Chunk<T>::V;
+    const auto on16 = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
+    CombineParams<T> p{};
+    p.z = static_cast<const T*>(a.z), p.weight = a.weight, p.ldz = a.ldz, p.n_rows = a.n_rows;
+    p.k = a.k, p.c = a.c, p.y = static_cast<T*>(a.y);
+    p.gy = static_cast<const T*>(a.gy), p.ldg = a.ldg, p.gz = static_cast<T*>(a.gz), p.gw = a.gw;
+    p.vec = a.c % V == 0 && a.ldz % V == 0 && a.ldg % V == 0 && on16(a.z) && on16(a.y) &&
+            on16(a.gy) && on16(a.gz);
+    return p;
+}
+
+template <typename T, int L>
+hipError_t run(const CombineArgs& a, hipStream_t stream) {
+    constexpr int V = Chunk<T>::V, kRows = kThreads / L;
+    CombineParams<T> p = params<T>(a);
+    p.blocks = ((a.c + V - 1) / V + L - 1) / L;
+    const int64_t grid = (a.n_rows + kRows - 1) / kRows * p.blocks;
+    return launch_ranges(grid, kThreads, [&](int64_t first, int64_t count) {
+        p.block0 = first;
+        zs_combine_kernel<T, L><<<unsigned(count), kThreads, 0, stream>>>(p);
+        return hipGetLastError();
+    });
+}
+
+template <typename T>
+hipError_t dispatch(const CombineArgs& a, hipStream_t stream) {
+    const int chunks = (a.c + Chunk<T>::V - 1) / Chunk<T>::V;
+    if (chunks <= 1) return run<T, 1>(a, stream);
+    if (chunks <= 2) return run<T, 2>(a, stream);
+    if (chunks <= 4) return run<T, 4>(a, stream);
+    if (chunks <= 8) return run<T, 8>(a, stream);
+    if (chunks <= 16) return run<T, 16>(a, stream);
+    if (chunks <= 32) return run<T, 32>(a, stream);
+    return run<T, 64>(a, stream);
+}
+
+template <typename T, int L, int NV>
+hipError_t run_bwd(const CombineArgs& a, hipStream_t stream) {
+    constexpr int kRows = threads_of(L) / L;
+    const CombineParams<T> p = params<T>(a);
+    const int64_t want = (a.n_rows + kRows - 1) / kRows;
+    zs_combine_bwd_kernel<T, L, NV>
+        <<<unsigned(want < 8192 ? want : 8192), threads_of(L), 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t dispatch_bwd(const CombineArgs& a, hipStream_t stream) {
+    const int chunks = (a.c + Chunk<T>::V - 1) / Chunk<T>::V;
+    if (chunks <= 1) return run_bwd<T, 1, 1>(a, stream);
+    if (chunks <= 2) return run_bwd<T, 2, 1>(a, stream);
+    if (chunks <= 4) return run_bwd<T, 4, 1>(a, stream);
+    if (chunks <= 8) return run_bwd<T, 8, 1>(a, stream);
+    if (chunks <= 16) return run_bwd<T, 16, 1>(a, stream);
+    if (chunks <= 32) return run_bwd<T, 32, 1>(a, stream);
+    if (chunks <= 64) return run_bwd<T, 64, 1>(a, stream);
+    if (chunks <= 128) return run_bwd<T, 64, 2>(a, stream);
+    if (chunks <= 256) return run_bwd<T, 64, 4>(a, stream);
+    if (chunks <= 512) return run_bwd<T, 256, 2>(a, stream);
+    if (chunks <= 1024) return run_bwd<T, 256, 4>(a, stream);
+    return run_bwd<T, 512, 4>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_combine(const CombineArgs& a, bool bf16, hipStream_t stream) {
+    return bf16 ? dispatch<__bf16>(a, stream) : dispatch<float>(a, stream);
+}
+
+hipError_t launch_combine_backward(const CombineArgs& a, bool bf16, hipStream_t stream) {
+    return bf16 ? dispatch_bwd<__bf16>(a, stream) : dispatch_bwd<float>(a, stream);
+}
+
+}  // namespace zs

@@ -1,0 +1,382 @@
+"""Binding of the operators before, between and behind the products of a block of experts (C ABI in
+``include/zs_layers.h``):
+
+* ``zs_embedding(table, index, scale)`` -> y, ``zs_embedding_backward(grad_y, index, n_entries, scale, groups)``, and
+  the autograd function ``embedding``: rows looked up by token or species; the gradient sums them in sorted order.
+* ``zs_layer_norm(x, w, b, eps)`` -> y, ``zs_layer_norm_backward``, and the autograd function ``layer_norm``.
+* ``Router(n_experts, k, ...)``, ``zs_route(logits, router, bias)`` -> (weight, expert), ``zs_route_backward``, the
+  autograd function ``route``, and ``expert_groups(expert, n_experts)``, the groups that ``grouped_mm`` reads.
+* ``zs_combine(z, weight)`` -> y, ``zs_combine_backward``, and the autograd function ``combine``: the weighted sum of
+  the experts' rows of a token.
+
+As in the rest of the package these functions only marshal arguments; there is no CPU fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+import os
+
+import torch
+
+from . import HEADER_PATH, Csr, _call, _check, _ptr, load, zs_build_csr
+from .block import DTYPES, _check_groups, _rows, _typed
+
+LAYERS_HEADER_PATH = os.path.join(os.path.dirname(HEADER_PATH), "zs_layers.h")
+MAX_LAYER_WIDTH, MAX_EXPERTS, MAX_SLOTS, MAX_EXPERT_GROUPS = 8192, 1024, 64, 64
+
+_layers_lib = None
+
+
+class _Router(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_int32), ("sigmoid", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("best", ctypes.c_int32),
+                ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+def load_layers() -> ctypes.CDLL:
+    """libzs.so with the signatures of include/zs_layers.h."""
+    global _layers_lib
+    if _layers_lib is None:
+        lib = load()
+        P, I64, SZ, INT, F32 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int,
+                                ctypes.c_float)
+        R = ctypes.POINTER(_Router)
+        sigs = {
+            "zs_embedding": ([P, I64, P, I64, I64, I64, F32, INT, P, P], INT),
+            "zs_embedding_backward_workspace_bytes": ([I64, I64, INT], SZ),
+            "zs_embedding_backward": ([P, I64, P, P, P, I64, I64, I64, F32, INT, P, P, SZ, P], INT),
+            "zs_layer_norm": ([P, I64, P, P, I64, I64, F32, INT, P, P], INT),
+            "zs_layer_norm_workspace_bytes": ([I64, I64], SZ),
+            "zs_layer_norm_backward": ([P, I64, P, I64, P, I64, I64, F32, INT, P, P, P, P, SZ, P],
+                                       INT),
+            "zs_route": ([P, I64, P, R, I64, I64, INT, P, P, P], INT),
+            "zs_route_backward": ([P, P, I64, P, R, I64, I64, INT, P, P], INT),
+            "zs_combine": ([P, I64, P, I64, I64, I64, INT, P, P], INT),
+            "zs_combine_backward": ([P, I64, P, I64, P, I64, I64, I64, INT, P, P, P], INT),
+        }
+        for name, (args, res) in sigs.items():
+            fn = getattr(lib, name)
+            fn.argtypes, fn.restype = args, res
+        _layers_lib = lib
+    return _layers_lib
+
+
+def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype | None = None,
+            device: torch.device | None = None) -> torch.Tensor:
+    """A checked matrix with contiguous rows."""
+    if _typed(t, name, dtype, device).dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    return _rows(t)
+
+
+def _dense(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype,
+           device: torch.device) -> torch.Tensor:
+    """A checked tensor of one shape, contiguous."""
+    if tuple(_typed(t, name, dtype, device).shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _stride(t: torch.Tensor) -> int:
+    """Row stride of a matrix with contiguous rows (a single row's says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _workspace(size: int, device: torch.device) -> torch.Tensor | None:
+    return torch.empty(size, dtype=torch.uint8, device=device) if size else None
+
+
+# ---- lookup ----------------------------------------------------------------------------------------
+
+def _index(index: torch.Tensor, device: torch.device) -> torch.Tensor:
+    if _typed(index, "index", torch.int64, device).dim() != 1:
+        raise ValueError("index must be (M,)")
+    return index if index.is_contiguous() else index.contiguous()
+
+
+def zs_embedding(table: torch.Tensor, index: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
+    """y (M, c) with y[i] = scale * table[index[i]]; table (V, c) float32 or
+    bfloat16, index (M,) int64.  The table may have a row stride.  Indices
+    outside [0, V) (padding) give zeros."""
+    table = _matrix(table, "table")
+    index = _index(index, table.device)
+    M, (V, c) = index.shape[0], table.shape
+    y = torch.empty((M, c), dtype=table.dtype, device=table.device)
+    _check("zs_embedding", _call(
+        table.device, load_layers().zs_embedding, _ptr(table), _stride(table), _ptr(index), M, V, c,
+        scale, DTYPES[table.dtype], _ptr(y)))
+    return y
+
+
+def zs_embedding_backward(grad_y: torch.Tensor, index: torch.Tensor, n_entries: int,
+                          scale: float = 1.0, groups: Csr | None = None) -> torch.Tensor:
+    """grad_table (n_entries, c) of zs_embedding, of grad_y's type: the rows of
+    each entry added in fp32 in increasing order, zeros for entries without any.
+
+    The sorted order is ``groups``: the ``Csr`` of ``zs_build_csr(index,
+    n_entries)`` or, for rows that already are in the order of their entries,
+    ``sorted_groups(offsets)``; without it the CSR is built here, without a
+    synchronisation."""
+    grad_y = _matrix(grad_y, "grad_y")
+    dev, (M, c) = grad_y.device, grad_y.shape
+    index = _index(index, dev)
+    if index.shape[0] != M:
+        raise ValueError(f"index must be ({M},)")
+    if groups is None:
+        bad = torch.empty(1, dtype=torch.int32, device=dev)   # padding is allowed: nobody looks
+        groups = zs_build_csr(index, n_entries, bad_flag=bad, order=False)
+    else:
+        if groups.n_nodes != n_entries:
+            raise ValueError(f"groups must be of {n_entries} entries")
+        _check_groups(groups, M, dev)
+    out = torch.empty((n_entries, c), dtype=grad_y.dtype, device=dev)
+    lib, dtype = load_layers(), DTYPES[grad_y.dtype]
+    size = lib.zs_embedding_backward_workspace_bytes(M, c, dtype)
+    ws = _workspace(size, dev)
+    _check("zs_embedding_backward", _call(
+        dev, lib.zs_embedding_backward, _ptr(grad_y), _stride(grad_y), _ptr(index),
+        _ptr(groups.rowptr), _ptr(groups.perm), M, n_entries, c, scale, dtype, _ptr(out), _ptr(ws),
+        size))
+    return out
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, table, index, scale, rowptr, perm):
+        ctx.save_for_backward(index, rowptr, perm)
+        ctx.scale, ctx.n_entries = scale, table.shape[0]
+        return zs_embedding(table, index, scale)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_y):
+        index, rowptr, perm = ctx.saved_tensors
+        groups = None if rowptr is None else Csr(rowptr, perm, None, ctx.n_entries)
+        return zs_embedding_backward(grad_y, index, ctx.n_entries, ctx.scale, groups), *(None,) * 4
+
+
+def embedding(table: torch.Tensor, index: torch.Tensor, scale: float = 1.0,
+              groups: Csr | None = None) -> torch.Tensor:
+    """Differentiable zs_embedding (no double backward); ``groups`` as in
+    zs_embedding_backward, where the caller has them already."""
+    if groups is not None and groups.n_nodes != table.shape[0]:
+        raise ValueError(f"groups must be of {table.shape[0]} entries")
+    return _Embedding.apply(table, index, scale, groups and groups.rowptr, groups and groups.perm)
+
+
+# ---- layer norm --------------------------------------------------------------------------------------
+
+def zs_layer_norm(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = None,
+                  eps: float = 1e-5) -> torch.Tensor:
+    """y = (x - mean) / sqrt(variance + eps) * w + b over the last of (M, c).
+    x is float32 or bfloat16 and may have a row stride; w and b are float32 (c,)."""
+    x = _matrix(x, "x")
+    dev, (M, c) = x.device, x.shape
+    w = _dense(w, "w", (c,), torch.float32, dev)
+    b = b if b is None else _dense(b, "b", (c,), torch.float32, dev)
+    y = torch.empty((M, c), dtype=x.dtype, device=dev)
+    _check("zs_layer_norm", _call(
+        dev, load_layers().zs_layer_norm, _ptr(x), _stride(x), _ptr(w), _ptr(b), M, c, eps,
+        DTYPES[x.dtype], _ptr(y)))
+    return y
+
+
+def zs_layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
+                           need_b: bool = True, eps: float = 1e-5):
+    """(grad_x, grad_w, grad_b) of zs_layer_norm; grad_b is None unless ``need_b``."""
+    x = _matrix(x, "x")
+    dev, (M, c) = x.device, x.shape
+    grad_y = _matrix(grad_y, "grad_y", x.dtype, dev)
+    if grad_y.shape != x.shape:
+        raise ValueError("grad_y must have x's shape")
+    w = _dense(w, "w", (c,), torch.float32, dev)
+    gx = torch.empty((M, c), dtype=x.dtype, device=dev)
+    gw, gb = torch.empty((2, c), dtype=torch.float32, device=dev).unbind(0)
+    gb = gb if need_b else None
+    lib = load_layers()
+    size = lib.zs_layer_norm_workspace_bytes(M, c)
+    ws = _workspace(size, dev)
+    _check("zs_layer_norm_backward", _call(
+        dev, lib.zs_layer_norm_backward, _ptr(grad_y), _stride(grad_y), _ptr(x), _stride(x),
+        _ptr(w), M, c, eps, DTYPES[x.dtype], _ptr(gx), _ptr(gw), _ptr(gb), _ptr(ws), size))
+    return gx, gw, gb
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, b, eps):
+        ctx.save_for_backward(x, w)
+        ctx.has_b, ctx.eps = b is not None, eps
+        return zs_layer_norm(x, w, b, eps)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_y):
+        x, w = ctx.saved_tensors
+        return (*zs_layer_norm_backward(grad_y, x, w, ctx.has_b, ctx.eps), None)
+
+
+def layer_norm(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = None,
+               eps: float = 1e-5) -> torch.Tensor:
+    """Differentiable zs_layer_norm (no double backward)."""
+    return _LayerNorm.apply(x, w, b, eps)
+
+
+# ---- routing -----------------------------------------------------------------------------------------
+
+class Router:
+    """How rows choose their experts (include/zs_layers.h has the definition).
+
+    ``score``: "softmax" or "sigmoid" of the logits.  ``groups``: the experts
+    in that many groups of consecutive ones, of which the ``top_groups`` stay
+    whose ``best`` (1 or 2) largest scores have the largest sum.  ``k``
+    experts are chosen from those; their scores are the weights, divided by
+    their sum if ``renormalise``, times ``scale``."""
+
+    def __init__(self, n_experts: int, k: int, score: str = "softmax", groups: int = 1,
+                 top_groups: int = 1, best: int = 2, renormalise: bool = True, scale: float = 1.0):
+        if score not in ("softmax", "sigmoid"):
+            raise ValueError("score must be 'softmax' or 'sigmoid'")
+        if not 1 <= n_experts <= MAX_EXPERTS:
+            raise ValueError(f"n_experts must be 1 to {MAX_EXPERTS}")
+        if not 1 <= groups <= MAX_EXPERT_GROUPS or n_experts % groups:
+            raise ValueError(f"groups must be 1 to {MAX_EXPERT_GROUPS} and divide n_experts")
+        if not 1 <= top_groups <= groups:
+            raise ValueError("top_groups must be 1 to groups")
+        if not 1 <= k <= min(MAX_SLOTS, n_experts // groups * top_groups):
+            raise ValueError(f"k must be 1 to {MAX_SLOTS} and at most the experts that stay")
+        if best not in (1, 2):
+            raise ValueError("best must be 1 or 2")
+        if not math.isfinite(scale):
+            raise ValueError("scale must be finite")
+        self.n_experts, self.k, self.score, self.groups = n_experts, k, score, groups
+        self.top_groups, self.best, self.renormalise, self.scale = (top_groups, best,
+                                                                    bool(renormalise), scale)
+        self._c = _Router(k, score == "sigmoid", groups, top_groups, best, bool(renormalise), scale)
+
+
+def _logits(logits: torch.Tensor, router: Router) -> torch.Tensor:
+    logits = _matrix(logits, "logits")
+    if logits.shape[1] != router.n_experts:
+        raise ValueError(f"logits must be (M, {router.n_experts})")
+    return logits
+
+
+def zs_route(logits: torch.Tensor, router: Router, bias: torch.Tensor | None = None):
+    """(weight (M, k) float32, expert (M, k) int64) of logits (M, E), float32 or
+    bfloat16, with an optional bias (E,) float32 that has a part in the choice
+    only.  Experts with a logit or bias of -inf are not there; a slot that no
+    expert is left for holds E and weight 0."""
+    logits = _logits(logits, router)
+    dev, M, E = logits.device, logits.shape[0], router.n_experts
+    bias = bias if bias is None else _dense(bias, "bias", (E,), torch.float32, dev)
+    weight = torch.empty((M, router.k), dtype=torch.float32, device=dev)
+    expert = torch.empty((M, router.k), dtype=torch.int64, device=dev)
+    _check("zs_route", _call(
+        dev, load_layers().zs_route, _ptr(logits), _stride(logits), _ptr(bias), router._c, M, E,
+        DTYPES[logits.dtype], _ptr(weight), _ptr(expert)))
+    return weight, expert
+
+
+def zs_route_backward(grad_weight: torch.Tensor, logits: torch.Tensor, expert: torch.Tensor,
+                      router: Router) -> torch.Tensor:
+    """grad_logits (M, E) of zs_route from grad_weight (M, k) float32, the choice
+    ``expert`` held fixed."""
+    logits = _logits(logits, router)
+    dev, M, E = logits.device, logits.shape[0], router.n_experts
+    grad_weight = _dense(grad_weight, "grad_weight", (M, router.k), torch.float32, dev)
+    expert = _dense(expert, "expert", (M, router.k), torch.int64, dev)
+    out = torch.empty((M, E), dtype=logits.dtype, device=dev)
+    _check("zs_route_backward", _call(
+        dev, load_layers().zs_route_backward, _ptr(grad_weight), _ptr(logits), _stride(logits),
+        _ptr(expert), router._c, M, E, DTYPES[logits.dtype], _ptr(out)))
+    return out
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, bias, router):
+        weight, expert = zs_route(logits, router, bias)
+        ctx.save_for_backward(logits, expert)
+        ctx.router = router
+        ctx.mark_non_differentiable(expert)
+        return weight, expert
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_weight, _):
+        logits, expert = ctx.saved_tensors
+        return zs_route_backward(grad_weight, logits, expert, ctx.router), None, None
+
+
+def route(logits: torch.Tensor, router: Router, bias: torch.Tensor | None = None):
+    """Differentiable zs_route (no double backward): the weights carry gradients
+    to the logits, the choice and the bias carry none."""
+    return _Route.apply(logits, bias, router)
+
+
+def expert_groups(expert: torch.Tensor, n_experts: int) -> Csr:
+    """The groups of the (M, k) chosen experts for grouped_mm: row t * k + j
+    belongs to expert[t, j].  Slots without an expert are rows of no group, whose
+    products are zeros.  Built without a synchronisation."""
+    if _typed(expert, "expert", torch.int64).dim() != 2:
+        raise ValueError("expert must be (M, k)")
+    bad = torch.empty(1, dtype=torch.int32, device=expert.device)
+    csr = zs_build_csr(expert.reshape(-1), n_experts + 1, bad_flag=bad, order=False)
+    return Csr(csr.rowptr[:-1], csr.perm, csr.dst32, n_experts)
+
+
+# ---- weighted sum --------------------------------------------------------------------------------------
+
+def _slots(z: torch.Tensor, weight: torch.Tensor):
+    z = _matrix(z, "z")
+    if _typed(weight, "weight", torch.float32, z.device).dim() != 2:
+        raise ValueError("weight must be (M, k)")
+    if z.shape[0] != weight.numel():
+        raise ValueError("z must have a row for each of weight's entries")
+    return z, weight if weight.is_contiguous() else weight.contiguous()
+
+
+def zs_combine(z: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
+    """y (M, c) with y[t] = sum over j of weight[t, j] * z[t * k + j]; z (M * k, c)
+    float32 or bfloat16, which may have a row stride, weight (M, k) float32."""
+    z, weight = _slots(z, weight)
+    (M, k), c = weight.shape, z.shape[1]
+    y = torch.empty((M, c), dtype=z.dtype, device=z.device)
+    _check("zs_combine", _call(
+        z.device, load_layers().zs_combine, _ptr(z), _stride(z), _ptr(weight), M, k, c,
+        DTYPES[z.dtype], _ptr(y)))
+    return y
+
+
+def zs_combine_backward(grad_y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor):
+    """(grad_z (M * k, c), grad_weight (M, k) float32) of zs_combine."""
+    z, weight = _slots(z, weight)
+    (M, k), c = weight.shape, z.shape[1]
+    grad_y = _matrix(grad_y, "grad_y", z.dtype, z.device)
+    if tuple(grad_y.shape) != (M, c):
+        raise ValueError(f"grad_y must be ({M}, {c})")
+    gz = torch.empty((M * k, c), dtype=z.dtype, device=z.device)
+    gw = torch.empty((M, k), dtype=torch.float32, device=z.device)
+    _check("zs_combine_backward", _call(
+        z.device, load_layers().zs_combine_backward, _ptr(grad_y), _stride(grad_y), _ptr(z),
+        _stride(z), _ptr(weight), M, k, c, DTYPES[z.dtype], _ptr(gz), _ptr(gw)))
+    return gz, gw
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, z, weight):
+        ctx.save_for_backward(z, weight)
+        return zs_combine(z, weight)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_y):
+        return zs_combine_backward(grad_y, *ctx.saved_tensors)
+
+
+def combine(z: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
+    """Differentiable zs_combine (no double backward)."""
+    return _Combine.apply(z, weight)

@@ -105,9 +105,10 @@ size_t zs_csr_workspace_bytes(int64_t n_edges, int64_t n_nodes);
  *                                 reaches the end of the build, *bad_flag is 0 if
  *                                 every dst was in range and nonzero otherwise.
  *
- * Out-of-range destinations are never used as indices: the outputs are then
- * unspecified, but no memory outside them, the workspace and bad_flag is
- * written.
+ * Out-of-range destinations are never used as indices and belong to no node:
+ * rowptr counts the others alone, which are the first rowptr[n_nodes] entries
+ * of perm in their order; the rest of perm is not written, and dst32 is -1 for
+ * them.  (The synchronous call reports them as an error all the same.)
  */
 int zs_build_csr(const int64_t *dst, int64_t n_edges, int64_t n_nodes,
                  int32_t *rowptr, int32_t *perm, int32_t *dst32, int32_t *order,
