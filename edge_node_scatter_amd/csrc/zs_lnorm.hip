@@ -135,13 +135,16 @@ __global__ __launch_bounds__(threads_of(L)) void zs_lnorm_kernel(const NormParam
     }
 }
 
-// Workgroups of the backward on a compute unit: as many as the registers of a
-// lane's part of a row leave room for without spilling.
+// Wavefronts of the backward on a SIMD: as many as the registers of a lane's part of a
+// row (its values, both sums, and both inputs of this row and the next as they lie in
+// memory) leave room for without spilling.  Rows of 512 lanes take whole workgroups
+// of two wavefronts a SIMD: two of them where they fit (8192 x 8192 in bf16 95 us, 112
+// with one; in fp32 two would spill, 104 us against 92).
 template <typename T, int L, int NV>
 constexpr int resident() {
-    constexpr int held = NV * Chunk<T>::V;
-    if (L > 256) return 1;
-    return held <= 8 ? 4 : (held <= 16 ? 3 : 2);
+    constexpr int held = NV * (3 * Chunk<T>::V + 16);
+    if (L > 256) return held <= 80 ? 4 : 2;
+    return held <= 56 ? 4 : (held <= 120 ? 3 : 2);
 }
 
 // A lane's part of a row's inputs as they lie in memory, read once and past the
@@ -304,7 +307,7 @@ hipError_t run_kernels(const NormParams<T>& p, bool backward, hipStream_t stream
         return hipGetLastError();
     }
     // one round of workgroups that all run at once
-    constexpr int64_t cap = 256 * resident<T, L, NV>();
+    constexpr int64_t cap = 256 * resident<T, L, NV>() * 256 / threads_of(L);
     static_assert(cap <= kMaxPartials, "partial sums for every workgroup");
     const unsigned grid = unsigned(want < cap ? want : cap);
     if (grid > 0) {
@@ -351,10 +354,11 @@ hipError_t dispatch(const NormArgs& a, bool backward, hipStream_t stream) {
     if (chunks <= 128) return run<T, 64, 2>(a, backward, stream);
     if (chunks <= 192) return run<T, 64, 3>(a, backward, stream);
     if (chunks <= 256) return run<T, 64, 4>(a, backward, stream);
-    if (chunks <= 512) return run<T, 256, 2>(a, backward, stream);
     if constexpr (sizeof(T) == 2) {
+        if (chunks <= 512) return run<T, 256, 2>(a, backward, stream);
         return run<T, 512, 2>(a, backward, stream);
     } else {
+        if (chunks <= 512) return run<T, 256, 2>(a, backward, stream);
         if (chunks <= 1024) return run<T, 256, 4>(a, backward, stream);
         return run<T, 512, 4>(a, backward, stream);
     }
