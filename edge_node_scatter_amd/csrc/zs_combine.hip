@@ -24,6 +24,7 @@ struct CombineParams {
     int64_t ldz, n_rows, block0;
     int k, c, blocks;   // column blocks of L chunks
     bool vec;
+    bool stream;   // the backward's gradient goes past the caches
     T* y;
     const T* gy;
     int64_t ldg;
@@ -69,9 +70,14 @@ __global__ __launch_bounds__(kThreads) void zs_combine_kernel(const CombineParam
 
 constexpr int threads_of(int L) { return L > kThreads ? L : kThreads; }
 
-template <typename T, int L, int NV>
+// Rows on 16 bytes of whole chunks (WHOLE) have code without tests of single
+// channels.  U slots' rows are in flight while as many are used: they are asked for
+// before those results are stored, as a wait for a load waits for every store before
+// it.
+template <typename T, int L, int NV, bool WHOLE>
 __global__ __launch_bounds__(threads_of(L)) void zs_combine_bwd_kernel(const CombineParams<T> p) {
     constexpr int V = Chunk<T>::V, kRows = threads_of(L) / L, kWaves = L > 64 ? L / 64 : 1;
+    constexpr int U = NV > 2 ? 1 : 2;
     __shared__ float dots[kWaves > 1 ? kWaves * ZS_MAX_SLOTS : 1];
     const int l = threadIdx.x % L, slot = threadIdx.x / L;
     for (int64_t base = int64_t(blockIdx.x) * kRows; base < p.n_rows;
@@ -79,35 +85,68 @@ __global__ __launch_bounds__(threads_of(L)) void zs_combine_bwd_kernel(const Com
         const int64_t t = base + slot;
         const bool live = t < p.n_rows;
         const int c = live ? p.c : 0;
+        u32x4 next[U][NV];
+        float next_w[U];
+        const auto load = [&](int j0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t row = t * p.k + j0 + u;
+                const bool in = live && j0 + u < p.k;
+                next_w[u] = in ? p.weight[row] : 0.0f;
+#pragma unroll
+                for (int n = 0; n < NV; ++n)
+                    next[u][n] = load_chunk<T, true>(p.z + row * p.ldz, l + n * L, in ? c : 0, WHOLE);
+            }
+        };
         float g[NV][V];
 #pragma unroll
         for (int n = 0; n < NV; ++n)
-            Chunk<T>::unpack(load_chunk(p.gy + t * p.ldg, l + n * L, c, p.vec), g[n]);
+            Chunk<T>::unpack(load_chunk<T, true>(p.gy + t * p.ldg, l + n * L, c, WHOLE), g[n]);
+        load(0);
         if constexpr (kWaves > 1) __syncthreads();   // the last token's dots are read
-        for (int j = 0; j < p.k; ++j) {
-            const int64_t row = t * p.k + j;
-            const float w = live ? p.weight[row] : 0.0f;
-            u32x4 raw[NV];
+        for (int j0 = 0; j0 < p.k; j0 += U) {
+            u32x4 raw[U][NV];
+            float w[U], dot[U];
 #pragma unroll
-            for (int n = 0; n < NV; ++n)
-                raw[n] = load_chunk(p.z + row * p.ldz, l + n * L, c, p.vec);
-            float dot = 0.0f;
+            for (int u = 0; u < U; ++u) {
+                w[u] = next_w[u];
 #pragma unroll
-            for (int n = 0; n < NV; ++n) {
-                float z[V];
-                Chunk<T>::unpack(raw[n], z);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    dot = __builtin_fmaf(g[n][i], z[i], dot);
-                    z[i] = w * g[n][i];
-                }
-                if (live) store_any(p.gz + row * p.c, l + n * L, c, p.vec, Chunk<T>::pack(z));
+                for (int n = 0; n < NV; ++n) raw[u][n] = next[u][n];
             }
-            dot = lane_sum<(L < 64 ? L : 64)>(dot);
-            if constexpr (kWaves > 1) {
-                if ((threadIdx.x & 63) == 0) dots[(threadIdx.x >> 6) * ZS_MAX_SLOTS + j] = dot;
-            } else if (l == 0 && live) {
-                p.gw[row] = dot;
+            load(j0 + U);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t row = t * p.k + j0 + u;
+                const bool in = live && j0 + u < p.k;
+                dot[u] = 0.0f;
+#pragma unroll
+                for (int n = 0; n < NV; ++n) {
+                    const int at = l + n * L;
+                    float z[V];
+                    Chunk<T>::unpack(raw[u][n], z);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        dot[u] = __builtin_fmaf(g[n][i], z[i], dot[u]);
+                        z[i] = w[u] * g[n][i];
+                    }
+                    if (!in || at * V >= c) continue;
+                    if (WHOLE)
+                        store_chunk(p.gz + row * p.c, at, c, true, Chunk<T>::pack(z), p.stream);
+                    else
+                        store_any(p.gz + row * p.c, at, c, false, Chunk<T>::pack(z));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) dot[u] = lane_sum<(L < 64 ? L : 64)>(dot[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (j0 + u >= p.k) continue;
+                if constexpr (kWaves > 1) {
+                    if ((threadIdx.x & 63) == 0)
+                        dots[(threadIdx.x >> 6) * ZS_MAX_SLOTS + j0 + u] = dot[u];
+                } else if (l == 0 && live) {
+                    p.gw[t * p.k + j0 + u] = dot[u];
+                }
             }
         }
         if constexpr (kWaves > 1) {
@@ -132,6 +171,8 @@ CombineParams<T> params(const CombineArgs& a) {
     p.gy = static_cast<const T*>(a.gy), p.ldg = a.ldg, p.gz = static_cast<T*>(a.gz), p.gw = a.gw;
     p.vec = a.c % V == 0 && a.ldz % V == 0 && a.ldg % V == 0 && on16(a.z) && on16(a.y) &&
             on16(a.gy) && on16(a.gz);
+    // as in the join's backward: outputs that fill half of the memory-side cache alone
+    p.stream = a.n_rows * a.k * a.c * int64_t(sizeof(T)) >= (int64_t(128) << 20);
     return p;
 }
 
@@ -165,8 +206,11 @@ hipError_t run_bwd(const CombineArgs& a, hipStream_t stream) {
     constexpr int kRows = threads_of(L) / L;
     const CombineParams<T> p = params<T>(a);
     const int64_t want = (a.n_rows + kRows - 1) / kRows;
-    zs_combine_bwd_kernel<T, L, NV>
-        <<<unsigned(want < 8192 ? want : 8192), threads_of(L), 0, stream>>>(p);
+    const unsigned grid = unsigned(want < 8192 ? want : 8192);
+    if (p.vec)
+        zs_combine_bwd_kernel<T, L, NV, true><<<grid, threads_of(L), 0, stream>>>(p);
+    else
+        zs_combine_bwd_kernel<T, L, NV, false><<<grid, threads_of(L), 0, stream>>>(p);
     return hipGetLastError();
 }
 
