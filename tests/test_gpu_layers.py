@@ -106,7 +106,7 @@ def sorted_form(index, V):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("c", WIDTHS)
 def test_embedding_backward(dev, dtype, c):
-    for M, V in ((0, 5), (1, 1), (9, 300), (1500, 3), (2100, 70)):
+    for M, V in ((0, 5), (1, 1), (9, 300), (1500, 3), (2100, 70), (2100, 1024), (900, 1500)):
         say("embedding backward", dtype, M, V, c)
         g = gen(M + 7 * c)
         gy, index = mk(g, M, c, dtype=dtype), tokens(g, M, V, pad=M > 2)
