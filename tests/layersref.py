@@ -126,7 +126,9 @@ def shares(x, expert, r):
 def route_grad(gw, x, expert, r):
     """(gx, bound): the slots' parts are formed in 64 bits, a difference of terms of size p |g| and p sum |g| p whose
     roundings are 2^-53 each (up to 64 additions and a handful of products); a softmax's part of
-    every logit is a product of two rounded factors, and the two parts are added in fp32."""
+    every logit is a product of two rounded factors, and the two parts are added in fp32.  The softmax's exponentials are
+    fp32: one is off by an ulp and by |d| half ulps for the rounding of its argument d = x - max, and their sum by as
+    much on average (|d| < 7 there, see the router's test)."""
     x = x.double()
     E = x.shape[1]
     live = (expert >= 0) & (expert < E)
@@ -144,8 +146,9 @@ def route_grad(gw, x, expert, r):
     size = torch.zeros_like(out)
     if r.score == "softmax" and not r.renormalise:
         part = torch.where(live.any(1, keepdim=True), scores(x, False) * (g * s).sum(1, keepdim=True), 0.0)
-        size = part.abs()
-        out, size = out - part, size + out.abs()
+        d = x - x.amax(1, keepdim=True)
+        part_size = part.abs() * (8 + 7 + torch.where(d > -200, d.abs(), 0.0)) / 8   # below -200 the part is 0
+        out, size = out - part, part_size + 15 / 8 * out.abs()
     return out, lambda dtype: rounded(out, HALF * (8 * size + 4 * out.abs()) + wide, dtype)
 
 

@@ -31,15 +31,19 @@ def check(x, router, bias, dev, gw_seed=0, what=""):
     weight, expert = zs.zs_route(xd, router, bd)
     w_ref, e_ref = ref.route(x, router, bias)
     assert torch.equal(expert.cpu(), e_ref), (what, (expert.cpu() != e_ref).nonzero()[:3])
-    # formed in 64 bits, rounded to fp32 once
+    # formed in 64 bits, rounded to fp32 once.  Only a softmax's sum over all experts is one of fp32 exponentials: each
+    # is off by an ulp (2 half ulps) and by |d| half ulps for the rounding of its argument d = x - max; on average over
+    # the terms' sizes |d| is at most the logarithm of their number (the terms' entropy), below 7 for 1024.
+    sums = 9 * 2.0 ** -24 if router.score == "softmax" and not router.renormalise else 0.0
     got = weight.double().cpu()
     assert torch.equal(got.isnan(), w_ref.isnan()), what
-    assert ((got - w_ref).abs() <= (2.0 ** -24 + 1e-12) * w_ref.abs() + 1e-44).logical_or(w_ref.isnan()).all(), what
+    ok = ((got - w_ref).abs() <= (2.0 ** -24 + 1e-12 + sums) * w_ref.abs() + 1e-44) | w_ref.isnan()
+    assert bool(ok.all()), what
     gw = torch.randn(expert.shape, generator=torch.Generator().manual_seed(gw_seed))
     gx = zs.zs_route_backward(gw.to(dev), xd, expert, router).double().cpu()
     g_ref, bound = ref.route_grad(gw, x, e_ref, router)
     ok = ((gx - g_ref).abs() <= bound(x.dtype)) | (gx.isnan() & g_ref.isnan())
-    assert ok.all(), (what, ((gx - g_ref).abs() - bound(x.dtype)).max().item())
+    assert bool(ok.all()), (what, ((gx - g_ref).abs() - bound(x.dtype)).max().item())
     return weight, expert, gx
 
 
