@@ -10,8 +10,20 @@
 //   sigmoid:      dx_ij = a gw_j s_ij (1 - s_ij)
 //   softmax:      dx_e = [e chosen] a gw_j s_e - s_e sum_l a gw_l s_il
 //
-// A row lies in the registers of L lanes, NV consecutive experts each, so that of
-// equal values the lowest lane's first one has the lowest index.
+// A row lies in the registers of L lanes, NV consecutive experts each.  The choice has to
+// be that of fp64 sums (two experts may differ by less than fp32 holds), at the price of
+// fp32: fp32 sums pick the groups and some more candidates than there are slots, by
+// halving a range of keys and counting; only candidates are ranked in fp64.  Groups that
+// fp32 cannot tell, and candidates that may not be all, are settled in fp64 over the whole
+// row, which is slow and rare (with random logits a row in a thousand).
+//
+// Bound by vector instructions, some 550 a row at 256 experts.  Measured on MI355X:
+//  - 16384 rows of 256 experts in 8 groups, 8 slots, bf16: 24 us (8.4 MB are read, 1.6
+//    written: 2 us at a copy's rate).  All in fp64, a wavefront a row, the largest key
+//    by lane reductions: 48 us; fp32 checked by gaps, whole rows anew in fp64: 35
+//    (rows that went that way ended 15 us after the rest); 16 lanes a row: 30; 64: 33.
+//  - gradients of 8191 rows of 160 experts, 6 slots, fp32: 9 us (11 MB).
+#include "zs_launch.h"
 #include "zs_layers_internal.h"
 #include "zs_row.h"
 
@@ -27,8 +39,9 @@ struct RouteParams {
     const T* x;
     const float* bias;
     int64_t ldx, n_rows;
+    int64_t block0;   // number of the launch's first workgroup
     int n, k, groups, top_groups, best;
-    int group_factor;   // e * group_factor >> 20 is the group of expert e
+    int per_group, group_factor;   // e * group_factor >> 20 is the group of expert e
     bool sigmoid, renormalise;
     float scale;
     float* weight;
@@ -42,6 +55,10 @@ struct RouteParams {
 template <int CTRL>
 __device__ inline float from_lane(float v) {
     return dpp<CTRL>(v);
+}
+template <int CTRL>
+__device__ inline int from_lane(int v) {
+    return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true);
 }
 template <int CTRL>
 __device__ inline double from_lane(double v) {
@@ -66,6 +83,12 @@ __device__ inline void halves(float v, float& a, float& b) {
     uint32_t x, y;
     halves<WIDE>(__builtin_bit_cast(uint32_t, v), x, y);
     a = __builtin_bit_cast(float, x), b = __builtin_bit_cast(float, y);
+}
+template <bool WIDE>
+__device__ inline void halves(int v, int& a, int& b) {
+    uint32_t x, y;
+    halves<WIDE>(uint32_t(v), x, y);
+    a = int(x), b = int(y);
 }
 template <bool WIDE>
 __device__ inline void halves(double v, double& a, double& b) {
@@ -99,9 +122,26 @@ template <int L, typename V>
 __device__ inline V row_max(V v) {
     return over_row<L>(v, [](V a, V b) { return a > b ? a : b; });
 }
+// fp32 values as integers of the same order (zeros are +0 here): integers are compared
+// across lanes without the steps that keep a float's NaN rules.
+__device__ inline int key_of(float v) {
+    const int b = __builtin_bit_cast(int, v);
+    return b ^ (b >> 31 & 0x7fffffff);
+}
+__device__ inline float value_of(int k) {
+    return __builtin_bit_cast(float, k ^ (k >> 31 & 0x7fffffff));
+}
+template <int L>
+__device__ inline int row_max(int v) {
+    return over_row<L>(v, [](int a, int b) { return a > b ? a : b; });
+}
 template <int L>
 __device__ inline float row_max(float v) {
-    return over_row<L>(v, [](float a, float b) { return __builtin_fmaxf(a, b); });
+    return value_of(row_max<L>(key_of(v)));
+}
+template <int L>
+__device__ inline int row_add(int v) {
+    return over_row<L>(v, [](int a, int b) { return a + b; });
 }
 template <int L>
 __device__ inline double row_add(double v) {
@@ -115,9 +155,20 @@ __device__ inline uint64_t row_ballot(bool b) {
     return all >> ((threadIdx.x & 63) / L * L) & ((uint64_t(1) << (L & 63)) - 1);
 }
 
-// NV logits from an address of any alignment; zeros behind the row's end.
+// e^d for d <= 0, off by less than two ulps: 2^(d log2 e) with what the product's rounding
+// and the constant leave out.  Below e^-87 it is 0.
+__device__ inline float exp_below(float d) {
+    d = __builtin_fmaxf(d, -200.0f);   // the rest of the product stays a number
+    const float t = d * 1.44269502162933349609375f;
+    const float rest = __builtin_fmaf(d, 1.44269502162933349609375f, -t) +
+                       d * 1.925963033500e-8f;
+    const float e = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(e, rest * 0.693147180559945f, e);
+}
+
+// NV values from an address of any alignment; `fill` behind the row's end.
 template <typename T, int NV>
-__device__ inline void load_logits(const T* row, int at, int n, float (&x)[NV]) {
+__device__ inline void load_values(const T* row, int at, int n, float fill, float (&x)[NV]) {
     if (at + NV <= n) {
         T raw[NV];
         __builtin_memcpy(raw, row + at, sizeof raw);
@@ -125,7 +176,7 @@ __device__ inline void load_logits(const T* row, int at, int n, float (&x)[NV]) 
         for (int i = 0; i < NV; ++i) x[i] = float(raw[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) x[i] = at + i < n ? float(row[at + i]) : 0.0f;
+        for (int i = 0; i < NV; ++i) x[i] = at + i < n ? float(row[at + i]) : fill;
     }
 }
 
@@ -138,253 +189,409 @@ __device__ inline Best2 join(Best2 p, float a, float b) {
                  __builtin_fmaxf(__builtin_fminf(p.a, a), __builtin_fmaxf(p.b, b))};
 }
 
-// Bytes of LDS of a row: shares (8), logits (4) and indices (4) of the slots, and with
-// groups the experts' q (8), the groups' scores (8) and whether they stay (4).
-__host__ __device__ inline int row_bytes(int n, int k, int groups) {
-    return k * 16 + (groups > 1 ? n * 8 + (groups * 12 + 7) / 8 * 8 : 0);
+// A row's part of LDS: all experts' keys (4 bytes each), the candidates' keys and scores
+// in fp64 (8 each), the slots' scores (8), the groups' scores in fp32, or in fp64 (8), the
+// indices of candidates and slots (4 each) and whether the groups stay (4).
+constexpr int kSpare = 8;   // candidates beside the slots
+struct RowLds {
+    double *key, *chance, *share, *score;
+    float* keys;
+    int *candidate, *id, *stays;
+};
+template <int L, int NV>
+__host__ __device__ inline int row_bytes(int k, int groups) {
+    return (L * NV * 4 + (3 * k + 2 * kSpare + groups) * 8 + (2 * k + kSpare + groups) * 4 + 15) /
+           16 * 16;
+}
+template <int L, int NV>
+__device__ inline RowLds row_lds(char* mine, int k, int groups) {
+    RowLds r;
+    r.keys = reinterpret_cast<float*>(mine);   // on 16 bytes
+    r.key = reinterpret_cast<double*>(r.keys + L * NV);
+    r.chance = r.key + k + kSpare;
+    r.share = r.chance + k + kSpare;
+    r.score = r.share + k;
+    r.candidate = reinterpret_cast<int*>(r.score + groups);
+    r.id = r.candidate + k + kSpare;
+    r.stays = r.id + k;
+    return r;
 }
 
-// The k experts of largest key, by rounds: the row's largest key, from the lowest lane
-// and place that holds it.  The chosen indices and logits go to LDS, n where no key
-// is left.  Returns whether two keys that follow each other, up to the first that is not
-// chosen, are no further apart than tol (tol < 0: not asked).
-template <int L, int NV, typename K>
-__device__ inline bool choose(K (&key)[NV], const float (&x)[NV], int l, int n, int k, K tol,
-                              int* id, float* xs) {
-    constexpr K none = -K(kInf);
-    K best = none, before = K(kInf);
-    int at = 0;
-    const auto find = [&] {
-        best = key[0], at = 0;
+// Marks the row's largest keys, at least `take` of them and at most `room`: bit i of the
+// result is the lane's key[i].  Where equal keys leave no such choice, exactly `take`, of
+// the equal ones those of lowest index.  The key they start at is found by halving the
+// range between the row's largest and smallest and counting; the middle is taken of the
+// values at first, which is quick for values of one size, and then of their bit
+// patterns, which ends after 32 steps for any.  take <= have, the keys above -inf, and
+// take <= room.  least_marked: no marked key is below it, no other one above it, and none
+// at it unless +inf is returned (equal keys were told apart by their index).
+template <int L, int NV>
+__device__ inline uint32_t mark_largest(const float (&key)[NV], int l, int have, int take, int room,
+                                        float& least_marked) {
+    float most = key[0], least = key[0] > -kInf ? key[0] : kInf;
 #pragma unroll
-        for (int i = 1; i < NV; ++i)
-            if (key[i] > best) best = key[i], at = i;
-    };
-    find();
-    bool close = false;
-    for (int r = 0; r < k; ++r) {
-        const K m = row_max<L>(best);
-        if (tol >= K(0)) close |= before - m <= tol;
-        before = m;
-        const uint64_t who = row_ballot<L>(best == m && m > none);
-        const int lane = who ? __builtin_ctzll(who) : -1;
-        if (l == lane) {
-            id[r] = l * NV + at;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (i == at) xs[r] = x[i], key[i] = none;
-            find();
-        }
-        if (lane < 0 && l == 0) id[r] = n, xs[r] = -kInf;
+    for (int i = 1; i < NV; ++i) {
+        most = __builtin_fmaxf(most, key[i]);
+        least = __builtin_fminf(least, key[i] > -kInf ? key[i] : kInf);
     }
-    if (tol >= K(0)) close |= before - row_max<L>(best) <= tol;
-    return close;
+    // at least `take` keys from lo on, fewer from hi on
+    int lo = -row_max<L>(-key_of(least)), hi = row_max<L>(key_of(most)) + 1, above = 0;
+    bool done = have <= room;
+    int bound = done ? lo : hi;   // the marked keys are those from here on ...
+    for (int step = 0; __ballot(!done) != 0; ++step) {
+        int mid = lo + int((uint32_t(hi) - uint32_t(lo)) >> 1);
+        if (step < 8) {   // uniform
+            const int m = key_of(0.5f * value_of(lo) + 0.5f * value_of(hi) + 0.0f);
+            if (m > lo && m < hi) mid = m;
+        }
+        const float t = value_of(mid);
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) c += key[i] >= t;
+        c = row_add<L>(c);
+        if (done) continue;
+        if (uint32_t(hi) - uint32_t(lo) <= 1) done = true;
+        else if (c > room) lo = mid;
+        else if (c >= take) bound = mid, above = take, done = true;
+        else hi = bound = mid, above = c;
+    }
+    uint32_t mask = 0;
+    const float from = value_of(bound);
+#pragma unroll
+    for (int i = NV - 1; i >= 0; --i) mask = mask + mask + (key[i] >= from ? 1 : 0);
+    // ... and as many as are missing of those one below, in the order of their index
+    const int missing = have <= room ? 0 : take - above;
+    least_marked = missing > 0 ? kInf : from;
+    if (__ballot(missing > 0)) {
+        const float tie = value_of(lo);
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) mine += key[i] == tie;
+        int before = mine;   // of lower lanes
+#pragma unroll
+        for (int d = 1; d < L; d *= 2) {
+            const int v = __shfl_up(before, d, L);
+            before += l >= d ? v : 0;
+        }
+        before -= mine;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (key[i] == tie && before < missing) ++before, mask |= 1u << i;
+    }
+    return mask;
+}
+
+// An expert's score in fp64.
+__device__ inline double score64(double x, bool sigmoid, double top, double total) {
+    return sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / total;
+}
+
+// A softmax's sum in fp64 (lean in registers, as few rows need it).
+template <typename T, int L>
+__device__ inline double total64(const T* logits, int n, double top, int l) {
+    double total = 0.0;
+#pragma unroll 1
+    for (int e = l; e < n; e += L) {
+        const double v = float(logits[e]);
+        total += v > -double(kInf) ? exp(v - top) : 0.0;
+    }
+    return row_add<L>(total);
+}
+
+// Which groups stay, from scores in fp64: for rows that fp32 cannot tell.
+template <typename T, int L>
+__device__ inline void groups64(const RouteParams<T>& p, const T* logits, int n, float top, int l,
+                                const RowLds& r) {
+    constexpr double none = -double(kInf);
+    const double total = p.sigmoid ? 1.0 : total64<T, L>(logits, n, top, l);
+    // a group at a time, as many lanes as there are at its experts
+    for (int g = 0; g < p.groups; ++g) {
+        double a = none, b = none;
+#pragma unroll 1
+        for (int i = l; i < p.per_group; i += L) {
+            const int e = g * p.per_group + i;
+            const double x = e < n ? double(float(logits[e])) : none;
+            const double bias = p.bias ? double(p.bias[e]) : 0.0;
+            const double q = x > none && bias > none
+                                 ? score64(x, p.sigmoid, top, total) + bias : none;
+            b = fmax(b, fmin(a, q));
+            a = fmax(a, q);
+        }
+        const double most = over_row<L>(a, [](double x, double y) { return x > y ? x : y; });
+        // the second is the largest of what is left once one lane has given its largest
+        const uint64_t who = row_ballot<L>(a == most);
+        const double rest = who && l == __builtin_ctzll(who) ? b : a;
+        const double next = over_row<L>(rest, [](double x, double y) { return x > y ? x : y; });
+        if (l == 0) r.score[g] = p.best == 2 && next > none ? most + next : most;
+    }
+    wave_lds_sync();
+    for (int g = l; g < p.groups; g += L) {
+        int before = 0;
+        const double v = r.score[g];
+        for (int h = 0; h < p.groups; ++h)
+            before += r.score[h] > v || (r.score[h] == v && h < g);
+        r.stays[g] = v > none && before < p.top_groups;
+    }
+    wave_lds_sync();
+}
+
+// The k experts of largest sum in fp64, by rounds over all of them: for rows with more
+// experts too close to call than there are candidates (as with equal logits and no bias
+// yet).
+template <typename T, int L>
+__device__ inline void choose64(const RouteParams<T>& p, const T* logits, int n, float top, int l,
+                                const RowLds& r) {
+    constexpr double none = -double(kInf);
+    const double total = p.sigmoid ? 1.0 : total64<T, L>(logits, n, top, l);
+    double last = double(kInf);   // the sum and index of the round before
+    int last_at = -1;
+    for (int j = 0; j < p.k; ++j) {
+        double best = none;
+        int at = p.n;
+#pragma unroll 1
+        for (int e = l; e < n; e += L) {
+            const double x = float(logits[e]), bias = double(p.bias[e]);
+            if (!(x > none && bias > none) || !(r.keys[e] > -kInf)) continue;
+            const double q = score64(x, p.sigmoid, top, total) + bias;
+            const bool left = q < last || (q == last && e > last_at);
+            if (left && q > best) best = q, at = e;   // (ties: the lane's lowest)
+        }
+        const double m = over_row<L>(best, [](double x, double y) { return x > y ? x : y; });
+        last_at = -row_max<L>(best == m && m > none ? -at : -p.n);
+        last = m;
+        if (l == 0) r.id[j] = last_at;
+        if (last_at == p.n) last = none;
+    }
+    wave_lds_sync();
+    for (int j = l; j < p.k; j += L)
+        r.share[j] = r.id[j] < p.n ? score64(float(logits[r.id[j]]), p.sigmoid, top, total) : 0.0;
+    wave_lds_sync();
 }
 
 template <typename T, int L, int NV>
 __global__ __launch_bounds__(kThreads) void zs_route_kernel(const RouteParams<T> p) {
-    extern __shared__ char lds[];
+    extern __shared__ __align__(16) char lds[];
     const int l = threadIdx.x % L, slot = threadIdx.x / L, e0 = l * NV;
-    char* mine = lds + slot * row_bytes(p.n, p.k, p.groups);
-    double* share = reinterpret_cast<double*>(mine);
-    double* q_of = share + p.k;
-    double* score = q_of + (p.groups > 1 ? p.n : 0);
-    float* xs = reinterpret_cast<float*>(score + (p.groups > 1 ? p.groups : 0));
-    int* id = reinterpret_cast<int*>(xs + p.k);
-    int* stays = id + p.k;
-    const int per = p.n / p.groups;
+    const RowLds r = row_lds<L, NV>(lds + slot * row_bytes<L, NV>(p.k, p.groups), p.k, p.groups);
+    float* group_score = reinterpret_cast<float*>(r.score);
     const bool ranked = p.bias || p.groups > 1;   // by more than the logits
-    for (int64_t base = int64_t(blockIdx.x) * (kThreads / L); base < p.n_rows;
-         base += int64_t(gridDim.x) * (kThreads / L)) {
-        const int64_t row = base + slot;
-        const bool live = row < p.n_rows;
-        float x[NV], b[NV];
-        bool there[NV];
-        bool bad = false;
-        float top = -kInf;
-        load_logits<T, NV>(p.x + row * p.ldx, e0, live ? p.n : 0, x);
-        if (p.bias) load_logits<float, NV>(p.bias, e0, p.n, b);
+    // lanes that hold a group, if whole lanes do and DPP joins them
+    const int lanes = p.per_group / NV;
+    const bool joined =
+        p.per_group % NV == 0 && lanes <= (L < 16 ? L : 16) && (lanes & (lanes - 1)) == 0;
+    float b[NV], bias_size = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) b[i] = 0.0f;
+    if (p.bias) {
+        load_values<float, NV>(p.bias, e0, p.n, 0.0f, b);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            bias_size = b[i] > -kInf ? __builtin_fmaxf(bias_size, __builtin_fabsf(b[i])) : bias_size;
+        bias_size = row_max<L>(bias_size);
+    }
+    const int64_t row = (p.block0 + blockIdx.x) * (kThreads / L) + slot;
+    const bool live = row < p.n_rows;
+    const int n = live ? p.n : 0;
+    const T* logits = p.x + row * p.ldx;
+    float x[NV];
+    bool bad = false;
+    load_values<T, NV>(logits, e0, n, -kInf, x);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        x[i] += 0.0f;   // -0 is +0, and no signalling NaN
+        bad |= x[i] != x[i];
+    }
+    float top = -kInf;
+    if (!p.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) top = __builtin_fmaxf(top, x[i]);
+        top = row_max<L>(top);
+        bad |= top == kInf;
+    }
+    bad = row_ballot<L>(bad) != 0;
+    // Sums of score and bias in fp32, and how far two of them may lie apart that fp64
+    // might order otherwise.  A score is off by at most 10 units of 2^-24 of the row's
+    // largest (softmax: two ulps of the exponential, the rounding of its argument d, of
+    // which e^-d d <= 0.37 counts, 4 for the sum and 3 for two products) or of 1
+    // (sigmoid: less), the sum by half an ulp; two of them, and some to spare.
+    float s[NV], most = 1.0f;
+    double total = 1.0;
+    if (!p.sigmoid && (ranked || !p.renormalise)) {
+        total = 0.0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            bad |= x[i] != x[i];
-            there[i] = live && e0 + i < p.n && x[i] > -kInf;
-            if (!there[i]) x[i] = -kInf;
-            if (p.bias) there[i] = there[i] && b[i] > -kInf;
-            else b[i] = 0.0f;
-            top = __builtin_fmaxf(top, x[i]);
+            s[i] = x[i] > -kInf ? exp_below(x[i] - top) : 0.0f;
+            total += double(s[i]);
         }
-        if (!p.sigmoid) {
-            top = row_max<L>(top);
-            bad |= top == kInf;
-        }
-        bad = row_ballot<L>(bad) != 0;
-        // scores in fp32, and how far two sums of a score and a bias may lie apart that
-        // fp64 might order otherwise
-        float s[NV], most = 1.0f;
-        double total = 1.0;
-        if (!p.sigmoid && (ranked || !p.renormalise)) {
-            total = 0.0;
+        total = row_add<L>(total);
+        most = total > 0.0 ? 1.0f / float(total) : 1.0f;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                s[i] = x[i] > -kInf ? expf(x[i] - top) : 0.0f;
-                total += double(s[i]);
+        for (int i = 0; i < NV; ++i) s[i] *= most;
+    } else if (ranked) {
+        // 2^(-x log2 e); what overflows or underflows in it leaves the score 0 or 1
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            s[i] = __builtin_amdgcn_rcpf(1.0f +
+                                         __builtin_amdgcn_exp2f(x[i] * -1.44269504088896341f));
+    }
+    const float tol = most * 0x1p-19f + (most + bias_size) * 0x1p-22f;
+    if (ranked)
+        // -inf or NaN where the bias is
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s[i] = x[i] > -kInf ? s[i] + b[i] : -kInf;
+    bool here = !bad;   // the lane's group stays, if it holds one
+    if (p.groups > 1) {
+        if (joined) {
+            Best2 t{-kInf, -kInf};
+#pragma unroll
+            for (int i = 0; i < NV; ++i) t = join(t, s[i], -kInf);
+            if (lanes >= 2) t = join(t, dpp<0xB1>(t.a), dpp<0xB1>(t.b));
+            if (lanes >= 4) t = join(t, dpp<0x4E>(t.a), dpp<0x4E>(t.b));
+            if (lanes >= 8) t = join(t, dpp<0x141>(t.a), dpp<0x141>(t.b));
+            if (lanes >= 16) t = join(t, dpp<0x140>(t.a), dpp<0x140>(t.b));
+            if (e0 < p.n)
+                group_score[e0 * p.group_factor >> 20] =
+                    p.best == 2 && t.b > -kInf ? t.a + t.b : t.a;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) r.keys[e0 + i] = s[i];
+            wave_lds_sync();
+            for (int g = l; g < p.groups; g += L) {
+                Best2 t{-kInf, -kInf};
+                for (int e = g * p.per_group; e < (g + 1) * p.per_group; ++e)
+                    t = join(t, r.keys[e], -kInf);
+                group_score[g] = p.best == 2 && t.b > -kInf ? t.a + t.b : t.a;
             }
-            total = row_add<L>(total);
-            most = total > 0.0 ? 1.0f / float(total) : 1.0f;
+        }
+        wave_lds_sync();
+        // a group stays if fewer than top_groups could be before it, and goes if as many
+        // surely are
+        bool close = false;
+        for (int g = l; g < p.groups; g += L) {
+            int could = 0, surely = 0;
+            const float v = group_score[g];
+            const float low = v - 2.0f * tol, high = v + 2.0f * tol;
+            for (int h = 0; h < p.groups; ++h) {
+                const float o = group_score[h];
+                could += o >= low;   // the group itself too
+                surely += o > high;
+            }
+            const bool some = v > -kInf;
+            r.stays[g] = some && could <= p.top_groups;
+            // (a bias of +inf leaves no bound)
+            close |= some && !(could <= p.top_groups || surely >= p.top_groups);
+            close |= !(tol < kInf);
+        }
+        wave_lds_sync();
+        if (__ballot(close && !bad)) groups64<T, L>(p, logits, n, top, l, r);
+        if (joined) here = here && e0 < p.n && r.stays[e0 * p.group_factor >> 20];
+    }
+    // the keys: sums, or logits without a bias
+    int have = 0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) s[i] *= most;
-        } else if (ranked) {
+    for (int i = 0; i < NV; ++i) {
+        bool on = here;
+        if (p.groups > 1) {
+            if (!joined)
+                on = on && r.stays[(e0 + i < p.n ? e0 + i : 0) * p.group_factor >> 20];
+            if (!p.bias) s[i] = s[i] > -kInf ? x[i] : -kInf;
+        } else if (!p.bias) {
+            s[i] = x[i];
+        }
+        s[i] = on ? s[i] : -kInf;
+        have += s[i] > -kInf;
+    }
+    wave_lds_sync();
 #pragma unroll
-            for (int i = 0; i < NV; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-x[i]));
+    for (int i = 0; i < NV; ++i) r.keys[e0 + i] = s[i];
+    have = row_add<L>(have);
+    // Candidates: with a bias two more than the slots at least, so that the first that is not
+    // one lies clearly behind the last slot.
+    const int room = p.k + kSpare, want = p.bias ? p.k + 2 : p.k;
+    float least;
+    uint32_t mask = mark_largest<L, NV>(s, l, have, have < want ? have : want, room, least);
+    int at = __builtin_popcount(mask);
+    const int mine = at;
+#pragma unroll
+    for (int d = 1; d < L; d *= 2) {
+        const int v = __shfl_up(at, d, L);
+        at += l >= d ? v : 0;
+    }
+    const int marked = __shfl(at, L - 1, L);
+    at -= mine;
+    for (; mask != 0; mask &= mask - 1) r.candidate[at++] = e0 + __builtin_ctz(mask);
+    wave_lds_sync();
+    // Their keys in fp64, and their places among each other.  In a softmax with a bias fp64
+    // scores need the sum in fp64 as well: where two lie close to each other, once more with
+    // that.
+    bool unsettled = false;   // what is no candidate may belong to the slots
+    for (int pass = 0;; ++pass) {
+        if (p.bias) {
+            for (int i = l; i < marked; i += L) {
+                const int e = r.candidate[i];
+                const double v = score64(float(logits[e]), p.sigmoid, top, total);
+                r.chance[i] = v;
+                r.key[i] = v + double(p.bias[e]);
+            }
+            wave_lds_sync();
         }
         bool close = false;
-        float key[NV];
-        float tol = -1.0f;
-        if (ranked) {
-            float size = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                s[i] = there[i] ? s[i] + b[i] : -kInf;
-                size = __builtin_fmaxf(size, there[i] ? __builtin_fabsf(s[i]) : 0.0f);
-            }
-            size = row_max<L>(size);
-            tol = most * 0x1p-19f + size * 0x1p-22f;
-            close = !(tol < kInf);
-        }
-        if (p.groups > 1) {
-            // lanes that hold a group, if whole lanes do and DPP joins them
-            const int lanes = per / NV;
-            float mine_score;
-            const bool whole = per % NV == 0 && lanes <= 16 && (lanes & (lanes - 1)) == 0;
-            float* score32 = reinterpret_cast<float*>(score);
-            if (whole) {
-                Best2 t{s[0], -kInf};
-#pragma unroll
-                for (int i = 1; i < NV; ++i) t = join(t, s[i], -kInf);
-                if (lanes >= 2) t = join(t, dpp<0xB1>(t.a), dpp<0xB1>(t.b));
-                if (lanes >= 4) t = join(t, dpp<0x4E>(t.a), dpp<0x4E>(t.b));
-                if (lanes >= 8) t = join(t, dpp<0x141>(t.a), dpp<0x141>(t.b));
-                if (lanes >= 16) t = join(t, dpp<0x140>(t.a), dpp<0x140>(t.b));
-                mine_score = p.best == 2 && t.b > -kInf ? t.a + t.b : t.a;
-                if (e0 < p.n) score32[e0 * p.group_factor >> 20] = mine_score;
-                wave_lds_sync();
+        unsettled = false;
+        for (int i = l; i < marked; i += L) {
+            const int e = r.candidate[i];
+            int rank = 0;
+            if (p.bias) {
+                const double own = r.key[i];
+                for (int j = 0; j < marked; ++j) {
+                    const double o = r.key[j];
+                    rank += o > own || (o == own && r.candidate[j] < e);
+                    close |= j != i && __builtin_fabs(o - own) <= double(tol);
+                }
+                unsettled |= rank == p.k - 1 && marked < have &&
+                             !(own >= double(least) + double(tol));
+                if (rank < p.k) r.share[rank] = r.chance[i];
             } else {
-                float* q32 = reinterpret_cast<float*>(q_of);
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (e0 + i < p.n) q32[e0 + i] = s[i];
-                wave_lds_sync();
-                for (int g = l; g < p.groups; g += L) {
-                    Best2 t{-kInf, -kInf};
-                    for (int e = g * per; e < (g + 1) * per; ++e) t = join(t, q32[e], -kInf);
-                    score32[g] = p.best == 2 && t.b > -kInf ? t.a + t.b : t.a;
+                const float own = r.keys[e];
+                for (int j = 0; j < marked; ++j) {
+                    const int f = r.candidate[j];
+                    const float o = r.keys[f];
+                    rank += o > own || (o == own && f < e);
                 }
-                wave_lds_sync();
             }
-            // a group stays if fewer than top_groups could be before it, and goes if as many
-            // surely are
-            for (int g = l; g < p.groups; g += L) {
-                int could = 0, surely = 0;
-                const float v = score32[g];
-                for (int h = 0; h < p.groups; ++h) {
-                    const float o = score32[h];
-                    could += h != g && o >= v - 2.0f * tol;
-                    surely += o > v + 2.0f * tol;
-                }
-                const bool some = v > -kInf;
-                stays[g] = some && could < p.top_groups;
-                close |= some && could >= p.top_groups && surely < p.top_groups;
-            }
-            wave_lds_sync();
+            if (rank < p.k) r.id[rank] = e;
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = e0 + i;
-            bool on = there[i] && !bad;
-            if (p.groups > 1) on = on && stays[(e < p.n ? e : 0) * p.group_factor >> 20];
-            key[i] = on ? (p.bias ? s[i] : x[i]) : -kInf;
-        }
-        close |= choose<L, NV, float>(key, x, l, p.n, p.k, p.bias ? tol : -1.0f, id, xs);
-        if (__ballot(close && ranked && !bad)) {
-            // some row of the wavefront is too close to call: scores in fp64
-            double q[NV], wide = 1.0;
-            if (!p.sigmoid) {
-                wide = 0.0;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    q[i] = x[i] > -kInf ? exp(double(x[i]) - double(top)) : 0.0;
-                    wide += q[i];
-                }
-                wide = row_add<L>(wide);
-            }
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                q[i] = p.sigmoid ? 1.0 / (1.0 + exp(-double(x[i]))) : q[i] / wide;
-                q[i] = there[i] ? q[i] + double(b[i]) : -double(kInf);
-            }
-            if (p.groups > 1) {
-                wave_lds_sync();
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (e0 + i < p.n) q_of[e0 + i] = q[i];
-                wave_lds_sync();
-                for (int g = l; g < p.groups; g += L) {
-                    double a = -double(kInf), c = -double(kInf);
-                    for (int e = g * per; e < (g + 1) * per; ++e) {
-                        const double v = q_of[e];
-                        c = fmax(c, fmin(a, v));
-                        a = fmax(a, v);
-                    }
-                    score[g] = p.best == 2 && c > -double(kInf) ? a + c : a;
-                }
-                wave_lds_sync();
-                for (int g = l; g < p.groups; g += L) {
-                    int before = 0;
-                    const double v = score[g];
-                    for (int h = 0; h < p.groups; ++h)
-                        before += score[h] > v || (score[h] == v && h < g);
-                    stays[g] = before < p.top_groups;
-                }
-                wave_lds_sync();
-            }
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int e = e0 + i;
-                bool on = there[i] && !bad;
-                if (p.groups > 1) on = on && stays[(e < p.n ? e : 0) * p.group_factor >> 20];
-                q[i] = on ? (p.bias ? q[i] : double(x[i])) : -double(kInf);
-            }
-            wave_lds_sync();
-            choose<L, NV, double>(q, x, l, p.n, p.k, -1.0, id, xs);
-        }
+        if (pass == 1 || !p.bias || p.sigmoid || __ballot(close) == 0) break;
+        total = total64<T, L>(logits, n, top, l);
         wave_lds_sync();
-        // weights from the chosen logits
-        float high = -kInf;
-        if (p.renormalise && !p.sigmoid)
-            for (int r = 0; r < p.k; ++r) high = __builtin_fmaxf(high, xs[r]);
-        for (int r = l; r < p.k; r += L) {
-            const double v = xs[r];
-            double w = 0.0;
-            if (id[r] < p.n) {
-                if (p.sigmoid) w = 1.0 / (1.0 + exp(-v));
-                else if (p.renormalise) w = exp(v - double(high));
-                else w = exp(v - double(top)) / total;
-            }
-            share[r] = w;
+    }
+    for (int j = marked + l; j < p.k; j += L) r.id[j] = p.n;
+    wave_lds_sync();
+    if (__ballot(unsettled)) choose64<T, L>(p, logits, n, top, l, r);
+    // the slots' scores or, renormalised in a softmax, exponentials above the largest chosen
+    if (!p.bias || (p.renormalise && !p.sigmoid)) {
+        float high = top;
+        if (p.renormalise && !p.sigmoid) {
+            high = -kInf;
+            for (int j = l; j < p.k; j += L)
+                if (r.id[j] < p.n) high = __builtin_fmaxf(high, float(logits[r.id[j]]));
+            high = row_max<L>(high);
         }
+        const double whole = p.renormalise ? 1.0 : total;
+        for (int j = l; j < p.k; j += L)
+            if (r.id[j] < p.n)
+                r.share[j] = score64(float(logits[r.id[j]]), p.sigmoid, high, whole);
         wave_lds_sync();
-        double sum = 1.0;
-        if (p.renormalise) {
-            sum = 0.0;
-            for (int r = 0; r < p.k; ++r) sum += share[r];
-        }
-        for (int r = l; r < p.k; r += L) {
-            if (!live) continue;
-            const float w = float(double(p.scale) * (sum > 0.0 ? share[r] / sum : 0.0));
-            p.weight[row * p.k + r] = bad ? __builtin_nanf("") : w;
-            p.expert[row * p.k + r] = id[r];
-        }
-        wave_lds_sync();   // before the next row's choice is written
+    }
+    double sum = 1.0;
+    if (p.renormalise) {
+        sum = 0.0;
+        for (int j = 0; j < p.k; ++j)
+            if (r.id[j] < p.n) sum += r.share[j];
+    }
+    for (int j = l; live && j < p.k; j += L) {
+        const double v = r.id[j] < p.n && sum > 0.0 ? r.share[j] / sum : 0.0;
+        p.weight[row * p.k + j] = bad ? __builtin_nanf("") : float(double(p.scale) * v);
+        p.expert[row * p.k + j] = r.id[j];
     }
 }
 
@@ -409,17 +616,14 @@ __global__ __launch_bounds__(kThreads) void zs_route_bwd_kernel(const RouteParam
         float top = -kInf;
         double total = 1.0;
         if (full) {
-            load_logits<T, NV>(x, l * NV, live ? p.n : 0, s);
+            load_values<T, NV>(x, l * NV, live ? p.n : 0, -kInf, s);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (l * NV + i >= p.n) s[i] = -kInf;
-                top = __builtin_fmaxf(top, s[i]);
-            }
+            for (int i = 0; i < NV; ++i) top = __builtin_fmaxf(top, s[i]);
             top = row_max<L>(top);
             total = 0.0;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                s[i] = l * NV + i < p.n ? expf(s[i] - top) : 0.0f;
+                s[i] = s[i] > -kInf ? exp_below(s[i] - top) : 0.0f;
                 total += double(s[i]);
             }
             total = row_add<L>(total);
@@ -499,20 +703,27 @@ hipError_t run(const RouteArgs& a, bool backward, hipStream_t stream) {
     p.x = static_cast<const T*>(a.x), p.bias = a.bias, p.ldx = a.ldx, p.n_rows = a.n_rows;
     p.n = a.n, p.k = a.r.k, p.groups = a.r.groups, p.top_groups = a.r.top_groups;
     p.best = a.r.best, p.sigmoid = a.r.sigmoid != 0, p.renormalise = a.r.renormalise != 0;
+    p.per_group = a.n / a.r.groups;
     // exact below 2^10 experts: the factor is less than one part in 2^20 / e too large
-    p.group_factor = ((1 << 20) + a.n / a.r.groups - 1) / (a.n / a.r.groups);
+    p.group_factor = ((1 << 20) + p.per_group - 1) / p.per_group;
     p.scale = a.r.scale, p.weight = a.weight, p.expert = a.expert;
     p.gw = a.gw, p.chosen = a.chosen, p.gx = static_cast<T*>(a.gx);
     constexpr int rows = kThreads / L;
     const int64_t want = (a.n_rows + rows - 1) / rows;
-    const unsigned grid = unsigned(want < 1 << 20 ? want : 1 << 20);
-    if (backward)
+    if (backward) {
+        const unsigned grid = unsigned(want < 1 << 20 ? want : 1 << 20);
         zs_route_bwd_kernel<T, L, NV>
             <<<grid, kThreads, size_t(rows) * back_bytes(p.k), stream>>>(p);
-    else
-        zs_route_kernel<T, L, NV>
-            <<<grid, kThreads, size_t(rows) * row_bytes(p.n, p.k, p.groups), stream>>>(p);
-    return hipGetLastError();
+        return hipGetLastError();
+    }
+    // (no loop over rows in the kernel: what the compiler took out of it cost as many registers
+    // again as the rows' own values)
+    return launch_ranges(want, kThreads, [&](int64_t first, int64_t count) {
+        p.block0 = first;
+        zs_route_kernel<T, L, NV><<<unsigned(count), kThreads,
+                                    size_t(rows) * row_bytes<L, NV>(p.k, p.groups), stream>>>(p);
+        return hipGetLastError();
+    });
 }
 
 template <typename T>
@@ -520,8 +731,8 @@ hipError_t dispatch(const RouteArgs& a, bool backward, hipStream_t stream) {
     if (a.n <= 8) return run<T, 8, 1>(a, backward, stream);
     if (a.n <= 32) return run<T, 8, 4>(a, backward, stream);
     if (a.n <= 64) return run<T, 16, 4>(a, backward, stream);
-    if (a.n <= 128) return run<T, 32, 4>(a, backward, stream);
-    if (a.n <= 256) return run<T, 64, 4>(a, backward, stream);
+    if (a.n <= 128) return run<T, 16, 8>(a, backward, stream);
+    if (a.n <= 256) return run<T, 32, 8>(a, backward, stream);
     if (a.n <= 512) return run<T, 64, 8>(a, backward, stream);
     return run<T, 64, 16>(a, backward, stream);
 }
