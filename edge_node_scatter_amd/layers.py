@@ -123,21 +123,32 @@ def zs_embedding_backward(grad_y: torch.Tensor, index: torch.Tensor, n_entries: 
     index = _index(index, dev)
     if index.shape[0] != M:
         raise ValueError(f"index must be ({M},)")
+    if n_entries < 1:
+        raise ValueError("n_entries must be positive")
+    out = torch.empty((n_entries, c), dtype=grad_y.dtype, device=dev)
+    lib, dtype = load_layers(), DTYPES[grad_y.dtype]
+    size = lib.zs_embedding_backward_workspace_bytes(M, c, dtype)
     if groups is None:
-        bad = torch.empty(1, dtype=torch.int32, device=dev)   # padding is allowed: nobody looks
-        groups = zs_build_csr(index, n_entries, bad_flag=bad, order=False)
+        # row offsets, order, entries, flag and workspaces in one allocation.  The flag says
+        # that there is padding, which is allowed: nobody looks at it.
+        need = int(lib.zs_csr_workspace_bytes(M, n_entries))
+        at, parts = 0, []
+        for part in (4 * (n_entries + 1), 4 * M, 4 * M, 4, need, size):
+            parts.append(at)
+            at += -(-part // 256) * 256
+        keep = torch.empty(at, dtype=torch.uint8, device=dev)
+        rowptr, perm, entries, flag, csr_ws, ws = (keep.data_ptr() + p for p in parts)
+        _check("zs_build_csr", _call(dev, lib.zs_build_csr, _ptr(index), M, n_entries, rowptr, perm,
+                                     entries, None, csr_ws, need, flag))
     else:
         if groups.n_nodes != n_entries:
             raise ValueError(f"groups must be of {n_entries} entries")
         _check_groups(groups, M, dev)
-    out = torch.empty((n_entries, c), dtype=grad_y.dtype, device=dev)
-    lib, dtype = load_layers(), DTYPES[grad_y.dtype]
-    size = lib.zs_embedding_backward_workspace_bytes(M, c, dtype)
-    ws = _workspace(size, dev)
+        keep = _workspace(size, dev)
+        rowptr, perm, ws = _ptr(groups.rowptr), _ptr(groups.perm), _ptr(keep)
     _check("zs_embedding_backward", _call(
-        dev, lib.zs_embedding_backward, _ptr(grad_y), _stride(grad_y), _ptr(index),
-        _ptr(groups.rowptr), _ptr(groups.perm), M, n_entries, c, scale, dtype, _ptr(out), _ptr(ws),
-        size))
+        dev, lib.zs_embedding_backward, _ptr(grad_y), _stride(grad_y), _ptr(index), rowptr, perm, M,
+        n_entries, c, scale, dtype, _ptr(out), ws, size))
     return out
 
 
