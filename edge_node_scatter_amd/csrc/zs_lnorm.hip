@@ -366,7 +366,12 @@ hipError_t dispatch(const NormArgs& a, bool backward, hipStream_t stream) {
 
 }  // namespace
 
+// Nothing where one workgroup holds all rows, whose sums are the gradients (a row's
+// lanes in fp32: in bf16 there are no more).
 size_t layer_norm_workspace(int64_t n_rows, int64_t c) {
+    int lanes = 1;
+    while (lanes < 64 && lanes * 4 < c) lanes *= 2;
+    if (n_rows <= (c <= 1024 ? 256 / lanes : 1)) return 0;
     const int64_t parts = n_rows < kMaxPartials ? n_rows : kMaxPartials;
     return size_t(parts * 2 * c * 4);
 }

@@ -63,24 +63,25 @@ def load_layers() -> ctypes.CDLL:
 
 
 def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype | None = None,
-            device: torch.device | None = None) -> torch.Tensor:
-    """A checked matrix with contiguous rows."""
+            device: torch.device | None = None):
+    """A checked matrix with contiguous rows, its shape and its row stride (a single
+    row's says nothing)."""
     if _typed(t, name, dtype, device).dim() != 2:
         raise ValueError(f"{name} must be a matrix")
-    return _rows(t)
+    if t.is_contiguous():   # the usual case
+        M, c = t.shape
+        return t, M, c, c
+    t = _rows(t)
+    M, c = t.shape
+    return t, M, c, t.stride(0) if M > 1 else c
 
 
 def _dense(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype,
            device: torch.device) -> torch.Tensor:
     """A checked tensor of one shape, contiguous."""
-    if tuple(_typed(t, name, dtype, device).shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}")
+    if _typed(t, name, dtype, device).shape != shape:   # (a torch.Size is a tuple)
+        raise ValueError(f"{name} must be {shape}")
     return t if t.is_contiguous() else t.contiguous()
-
-
-def _stride(t: torch.Tensor) -> int:
-    """Row stride of a matrix with contiguous rows (a single row's says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def _workspace(size: int, device: torch.device) -> torch.Tensor | None:
@@ -99,13 +100,14 @@ def zs_embedding(table: torch.Tensor, index: torch.Tensor, scale: float = 1.0) -
     """y (M, c) with y[i] = scale * table[index[i]]; table (V, c) float32 or
     bfloat16, index (M,) int64.  The table may have a row stride.  Indices
     outside [0, V) (padding) give zeros."""
-    table = _matrix(table, "table")
-    index = _index(index, table.device)
-    M, (V, c) = index.shape[0], table.shape
-    y = torch.empty((M, c), dtype=table.dtype, device=table.device)
+    table, V, c, stride = _matrix(table, "table")
+    dev = table.device
+    index = _index(index, dev)
+    M = index.shape[0]
+    y = table.new_empty((M, c))
     _check("zs_embedding", _call(
-        table.device, load_layers().zs_embedding, _ptr(table), _stride(table), _ptr(index), M, V, c,
-        scale, DTYPES[table.dtype], _ptr(y)))
+        dev, load_layers().zs_embedding, table.data_ptr(), stride, index.data_ptr(), M, V, c, scale,
+        DTYPES[table.dtype], y.data_ptr()))
     return y
 
 
@@ -118,14 +120,14 @@ def zs_embedding_backward(grad_y: torch.Tensor, index: torch.Tensor, n_entries: 
     n_entries)`` or, for rows that already are in the order of their entries,
     ``sorted_groups(offsets)``; without it the CSR is built here, without a
     synchronisation."""
-    grad_y = _matrix(grad_y, "grad_y")
-    dev, (M, c) = grad_y.device, grad_y.shape
+    grad_y, M, c, stride = _matrix(grad_y, "grad_y")
+    dev = grad_y.device
     index = _index(index, dev)
     if index.shape[0] != M:
         raise ValueError(f"index must be ({M},)")
     if n_entries < 1:
         raise ValueError("n_entries must be positive")
-    out = torch.empty((n_entries, c), dtype=grad_y.dtype, device=dev)
+    out = grad_y.new_empty((n_entries, c))
     lib, dtype = load_layers(), DTYPES[grad_y.dtype]
     size = lib.zs_embedding_backward_workspace_bytes(M, c, dtype)
     if groups is None:
@@ -147,7 +149,7 @@ def zs_embedding_backward(grad_y: torch.Tensor, index: torch.Tensor, n_entries: 
         keep = _workspace(size, dev)
         rowptr, perm, ws = _ptr(groups.rowptr), _ptr(groups.perm), _ptr(keep)
     _check("zs_embedding_backward", _call(
-        dev, lib.zs_embedding_backward, _ptr(grad_y), _stride(grad_y), _ptr(index), rowptr, perm, M,
+        dev, lib.zs_embedding_backward, _ptr(grad_y), stride, _ptr(index), rowptr, perm, M,
         n_entries, c, scale, dtype, _ptr(out), ws, size))
     return out
 
@@ -182,35 +184,35 @@ def zs_layer_norm(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = Non
                   eps: float = 1e-5) -> torch.Tensor:
     """y = (x - mean) / sqrt(variance + eps) * w + b over the last of (M, c).
     x is float32 or bfloat16 and may have a row stride; w and b are float32 (c,)."""
-    x = _matrix(x, "x")
-    dev, (M, c) = x.device, x.shape
+    x, M, c, stride = _matrix(x, "x")
+    dev = x.device
     w = _dense(w, "w", (c,), torch.float32, dev)
     b = b if b is None else _dense(b, "b", (c,), torch.float32, dev)
-    y = torch.empty((M, c), dtype=x.dtype, device=dev)
+    y = x.new_empty((M, c))
     _check("zs_layer_norm", _call(
-        dev, load_layers().zs_layer_norm, _ptr(x), _stride(x), _ptr(w), _ptr(b), M, c, eps,
-        DTYPES[x.dtype], _ptr(y)))
+        dev, load_layers().zs_layer_norm, x.data_ptr(), stride, w.data_ptr(), _ptr(b), M, c, eps,
+        DTYPES[x.dtype], y.data_ptr()))
     return y
 
 
 def zs_layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
                            need_b: bool = True, eps: float = 1e-5):
     """(grad_x, grad_w, grad_b) of zs_layer_norm; grad_b is None unless ``need_b``."""
-    x = _matrix(x, "x")
-    dev, (M, c) = x.device, x.shape
-    grad_y = _matrix(grad_y, "grad_y", x.dtype, dev)
-    if grad_y.shape != x.shape:
+    x, M, c, stride = _matrix(x, "x")
+    dev = x.device
+    grad_y, gM, gc, g_stride = _matrix(grad_y, "grad_y", x.dtype, dev)
+    if (gM, gc) != (M, c):
         raise ValueError("grad_y must have x's shape")
     w = _dense(w, "w", (c,), torch.float32, dev)
-    gx = torch.empty((M, c), dtype=x.dtype, device=dev)
-    gw, gb = torch.empty((2, c), dtype=torch.float32, device=dev).unbind(0)
-    gb = gb if need_b else None
+    gx, gw = x.new_empty((M, c)), w.new_empty(c)
+    gb = w.new_empty(c) if need_b else None
     lib = load_layers()
     size = lib.zs_layer_norm_workspace_bytes(M, c)
     ws = _workspace(size, dev)
     _check("zs_layer_norm_backward", _call(
-        dev, lib.zs_layer_norm_backward, _ptr(grad_y), _stride(grad_y), _ptr(x), _stride(x),
-        _ptr(w), M, c, eps, DTYPES[x.dtype], _ptr(gx), _ptr(gw), _ptr(gb), _ptr(ws), size))
+        dev, lib.zs_layer_norm_backward, grad_y.data_ptr(), g_stride, x.data_ptr(), stride,
+        w.data_ptr(), M, c, eps, DTYPES[x.dtype], gx.data_ptr(), gw.data_ptr(), _ptr(gb), _ptr(ws),
+        size))
     return gx, gw, gb
 
 
@@ -267,11 +269,11 @@ class Router:
         self._c = _Router(k, score == "sigmoid", groups, top_groups, best, bool(renormalise), scale)
 
 
-def _logits(logits: torch.Tensor, router: Router) -> torch.Tensor:
-    logits = _matrix(logits, "logits")
-    if logits.shape[1] != router.n_experts:
+def _logits(logits: torch.Tensor, router: Router):
+    logits, M, E, stride = _matrix(logits, "logits")
+    if E != router.n_experts:
         raise ValueError(f"logits must be (M, {router.n_experts})")
-    return logits
+    return logits, M, E, stride
 
 
 def zs_route(logits: torch.Tensor, router: Router, bias: torch.Tensor | None = None):
@@ -279,14 +281,14 @@ def zs_route(logits: torch.Tensor, router: Router, bias: torch.Tensor | None = N
     bfloat16, with an optional bias (E,) float32 that has a part in the choice
     only.  Experts with a logit or bias of -inf are not there; a slot that no
     expert is left for holds E and weight 0."""
-    logits = _logits(logits, router)
-    dev, M, E = logits.device, logits.shape[0], router.n_experts
+    logits, M, E, stride = _logits(logits, router)
+    dev = logits.device
     bias = bias if bias is None else _dense(bias, "bias", (E,), torch.float32, dev)
-    weight = torch.empty((M, router.k), dtype=torch.float32, device=dev)
-    expert = torch.empty((M, router.k), dtype=torch.int64, device=dev)
+    weight = logits.new_empty((M, router.k), dtype=torch.float32)
+    expert = logits.new_empty((M, router.k), dtype=torch.int64)
     _check("zs_route", _call(
-        dev, load_layers().zs_route, _ptr(logits), _stride(logits), _ptr(bias), router._c, M, E,
-        DTYPES[logits.dtype], _ptr(weight), _ptr(expert)))
+        dev, load_layers().zs_route, logits.data_ptr(), stride, _ptr(bias), router._c, M, E,
+        DTYPES[logits.dtype], weight.data_ptr(), expert.data_ptr()))
     return weight, expert
 
 
@@ -294,14 +296,14 @@ def zs_route_backward(grad_weight: torch.Tensor, logits: torch.Tensor, expert: t
                       router: Router) -> torch.Tensor:
     """grad_logits (M, E) of zs_route from grad_weight (M, k) float32, the choice
     ``expert`` held fixed."""
-    logits = _logits(logits, router)
-    dev, M, E = logits.device, logits.shape[0], router.n_experts
+    logits, M, E, stride = _logits(logits, router)
+    dev = logits.device
     grad_weight = _dense(grad_weight, "grad_weight", (M, router.k), torch.float32, dev)
     expert = _dense(expert, "expert", (M, router.k), torch.int64, dev)
-    out = torch.empty((M, E), dtype=logits.dtype, device=dev)
+    out = logits.new_empty((M, E))
     _check("zs_route_backward", _call(
-        dev, load_layers().zs_route_backward, _ptr(grad_weight), _ptr(logits), _stride(logits),
-        _ptr(expert), router._c, M, E, DTYPES[logits.dtype], _ptr(out)))
+        dev, load_layers().zs_route_backward, grad_weight.data_ptr(), logits.data_ptr(), stride,
+        expert.data_ptr(), router._c, M, E, DTYPES[logits.dtype], out.data_ptr()))
     return out
 
 
@@ -341,38 +343,37 @@ def expert_groups(expert: torch.Tensor, n_experts: int) -> Csr:
 # ---- weighted sum --------------------------------------------------------------------------------------
 
 def _slots(z: torch.Tensor, weight: torch.Tensor):
-    z = _matrix(z, "z")
+    """z, its width and row stride, weight and its shape, checked."""
+    z, rows, c, stride = _matrix(z, "z")
     if _typed(weight, "weight", torch.float32, z.device).dim() != 2:
         raise ValueError("weight must be (M, k)")
-    if z.shape[0] != weight.numel():
+    M, k = weight.shape
+    if rows != M * k:
         raise ValueError("z must have a row for each of weight's entries")
-    return z, weight if weight.is_contiguous() else weight.contiguous()
+    return z, c, stride, weight if weight.is_contiguous() else weight.contiguous(), M, k
 
 
 def zs_combine(z: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
     """y (M, c) with y[t] = sum over j of weight[t, j] * z[t * k + j]; z (M * k, c)
     float32 or bfloat16, which may have a row stride, weight (M, k) float32."""
-    z, weight = _slots(z, weight)
-    (M, k), c = weight.shape, z.shape[1]
-    y = torch.empty((M, c), dtype=z.dtype, device=z.device)
+    z, c, stride, weight, M, k = _slots(z, weight)
+    y = z.new_empty((M, c))
     _check("zs_combine", _call(
-        z.device, load_layers().zs_combine, _ptr(z), _stride(z), _ptr(weight), M, k, c,
-        DTYPES[z.dtype], _ptr(y)))
+        z.device, load_layers().zs_combine, z.data_ptr(), stride, weight.data_ptr(), M, k, c,
+        DTYPES[z.dtype], y.data_ptr()))
     return y
 
 
 def zs_combine_backward(grad_y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor):
     """(grad_z (M * k, c), grad_weight (M, k) float32) of zs_combine."""
-    z, weight = _slots(z, weight)
-    (M, k), c = weight.shape, z.shape[1]
-    grad_y = _matrix(grad_y, "grad_y", z.dtype, z.device)
-    if tuple(grad_y.shape) != (M, c):
+    z, c, stride, weight, M, k = _slots(z, weight)
+    grad_y, gM, gc, g_stride = _matrix(grad_y, "grad_y", z.dtype, z.device)
+    if (gM, gc) != (M, c):
         raise ValueError(f"grad_y must be ({M}, {c})")
-    gz = torch.empty((M * k, c), dtype=z.dtype, device=z.device)
-    gw = torch.empty((M, k), dtype=torch.float32, device=z.device)
+    gz, gw = z.new_empty((M * k, c)), weight.new_empty((M, k))
     _check("zs_combine_backward", _call(
-        z.device, load_layers().zs_combine_backward, _ptr(grad_y), _stride(grad_y), _ptr(z),
-        _stride(z), _ptr(weight), M, k, c, DTYPES[z.dtype], _ptr(gz), _ptr(gw)))
+        z.device, load_layers().zs_combine_backward, grad_y.data_ptr(), g_stride, z.data_ptr(),
+        stride, weight.data_ptr(), M, k, c, DTYPES[z.dtype], gz.data_ptr(), gw.data_ptr()))
     return gz, gw
 
 

@@ -99,9 +99,10 @@ def test_layer_norm_rejects(lib):
     for kw in (dict(y=A), dict(y=B + 32), dict(y=C)):
         assert f(**kw) == ALIAS, kw
     assert f(M=0) == 0
-    need = lib.zs_layer_norm_workspace_bytes(4, 16)
-    assert need > 0 and lib.zs_layer_norm_workspace_bytes(4, 0) == 0 and lib.zs_layer_norm_workspace_bytes(-1, 8) == 0
-    back = dict(gy=A, lg=16, x=B, ld=16, w=C, M=4, c=16, eps=1e-5, dt=0, gx=D, gw=E, gb=F, ws=G, nb=need, s=None)
+    need = lib.zs_layer_norm_workspace_bytes(400, 16)
+    assert need > 0 and lib.zs_layer_norm_workspace_bytes(1, 8192) == 0   # one workgroup's sums are the gradients
+    assert lib.zs_layer_norm_workspace_bytes(4, 0) == 0 and lib.zs_layer_norm_workspace_bytes(-1, 8) == 0
+    back = dict(gy=A, lg=16, x=B, ld=16, w=C, M=400, c=16, eps=1e-5, dt=0, gx=D, gw=E, gb=F, ws=G, nb=need, s=None)
 
     def g(**kw):
         return lib.zs_layer_norm_backward(*{**back, **kw}.values())
