@@ -98,7 +98,9 @@ __device__ inline Stats deviations(const u32x4 (&raw)[NV], float (&d)[NV][Chunk<
     row_sum<L>(q, lds, region);
     const float rest = q[0] * inv_c;
     Stats t;
-    t.r = 1.0f / sqrtf(__builtin_fmaf(q[1], inv_c, eps - rest * rest));
+    // (the difference of two rounded values can be below 0 where all deviations are the same)
+    const float var = __builtin_fmaf(q[1], inv_c, -rest * rest);
+    t.r = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps);
     t.shift = -rest * t.r;
     return t;
 }

@@ -330,9 +330,11 @@ def route(logits: torch.Tensor, router: Router, bias: torch.Tensor | None = None
 
 
 def expert_groups(expert: torch.Tensor, n_experts: int) -> Csr:
-    """The groups of the (M, k) chosen experts for grouped_mm: row t * k + j
-    belongs to expert[t, j].  Slots without an expert are rows of no group, whose
-    products are zeros.  Built without a synchronisation."""
+    """The groups of the (M, k) experts that zs_route chose, for grouped_mm: row
+    t * k + j belongs to expert[t, j].  Slots without an expert (index
+    ``n_experts``) are rows of no group, whose products are zeros.  Indices
+    outside [0, n_experts] are not looked for, as the groups are built without a
+    synchronisation: products of such rows, and of others, are unspecified."""
     if _typed(expert, "expert", torch.int64).dim() != 2:
         raise ValueError("expert must be (M, k)")
     bad = torch.empty(1, dtype=torch.int32, device=expert.device)

@@ -245,6 +245,12 @@ def test_layer_norm_of_odd_rows(dev):
         within(zs.zs_layer_norm(x.to(dev), w.to(dev), b.to(dev)), want, bound(F32), "scale")
         (gx, _, _), (bx, _, _) = ref.layer_norm_grads(gy[:x.shape[0]], x, w, 1e-5)
         within(zs.zs_layer_norm_backward(gy[:x.shape[0]].to(dev), x.to(dev), w.to(dev))[0], gx, bx(F32), "scale")
+    # constant rows whose sum is not exact: no spread, so nothing that is not a number
+    for v in (1.1e6, 7.3e9, 3.3e15):
+        for c in (30, 257, 777, 1031, 2048, 4100):
+            x, one = torch.full((5, c), v, device=dev), torch.ones(c, device=dev)
+            assert zs.zs_layer_norm(x, one).isfinite().all()
+            assert all(t.isfinite().all() for t in zs.zs_layer_norm_backward(torch.ones_like(x), x, one))
     y = zs.zs_layer_norm(torch.tensor([[5.0], [-2.0]], device=dev), torch.ones(1, device=dev), torch.full((1,), 0.25, device=dev))
     assert (y == 0.25).all()
     # what is not a number stays in its row
@@ -436,6 +442,78 @@ def test_other_stream(dev):
         got = run_all(a)
     s.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
+def test_two_streams_at_once(dev):
+    """Calls in flight on two streams have workspaces of their own."""
+    say("two streams")
+    a, b = inputs_of_all(dev, F32), inputs_of_all(dev, BF16)
+    want = [run_all(a), run_all(b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for i, x in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run_all(x))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for res in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(want[i], res))
+
+
+def test_outputs_end_where_they_should(dev):
+    """Through the C ABI, with marks before and behind every output."""
+    say("marks")
+    lib, g = layers.load_layers(), gen(31)
+
+    def marked(n, dtype=F32):
+        t = torch.full((n + 128,), 77, dtype=dtype, device=dev)
+        return t, t[64:].data_ptr()
+
+    def intact(*ts):
+        assert all((t[:64] == 77).all() and (t[-64:] == 77).all() and not (t[64:-64] == 77).any() for t in ts)
+    for dtype, code in ((F32, 0), (BF16, 1)):
+        for M, c, k in ((37, 33, 3), (70, 64, 2), (5, 1031, 7), (9, 4100, 2)):
+            x, gy, w = mk(g, M * k, c, dtype=dtype).to(dev), mk(g, M * k, c, dtype=dtype).to(dev), mk(g, c).to(dev)
+            index = torch.randint(0, 50, (M * k,), generator=g).to(dev)
+            groups = zs.zs_build_csr(index, 50)
+            y, at = marked(M * k * c, dtype)
+            assert zs._call(dev, lib.zs_embedding, x.data_ptr(), c, (index % (M * k)).data_ptr(), M * k, M * k, c, 1.0, code, at) == 0
+            t, t_at = marked(50 * c, dtype)
+            size = lib.zs_embedding_backward_workspace_bytes(M * k, c, code)
+            ws2 = torch.full((size + 512,), 77, dtype=torch.uint8, device=dev)
+            assert zs._call(dev, lib.zs_embedding_backward, gy.data_ptr(), c, index.data_ptr(), groups.rowptr.data_ptr(), groups.perm.data_ptr(), M * k, 50, c, 1.0, code, t_at, ws2.data_ptr(), size) == 0
+            n, n_at = marked(M * c, dtype)
+            assert zs._call(dev, lib.zs_layer_norm, x.data_ptr(), c, w.data_ptr(), None, M, c, 1e-5, code, n_at) == 0
+            gx, gx_at = marked(M * c, dtype)
+            gw, gw_at = marked(c)
+            gb, gb_at = marked(c)
+            size2 = lib.zs_layer_norm_workspace_bytes(M, c)
+            ws3 = torch.full((size2 + 512,), 77, dtype=torch.uint8, device=dev)
+            assert zs._call(dev, lib.zs_layer_norm_backward, gy.data_ptr(), c, x.data_ptr(), c, w.data_ptr(), M, c, 1e-5, code, gx_at, gw_at, gb_at, ws3.data_ptr(), size2) == 0
+            weight = torch.rand(M, k, generator=g).to(dev)
+            s, s_at = marked(M * c, dtype)
+            assert zs._call(dev, lib.zs_combine, x.data_ptr(), c, weight.data_ptr(), M, k, c, code, s_at) == 0
+            gz, gz_at = marked(M * k * c, dtype)
+            gv, gv_at = marked(M * k)
+            assert zs._call(dev, lib.zs_combine_backward, gy.data_ptr(), c, x.data_ptr(), c, weight.data_ptr(), M, k, c, code, gz_at, gv_at) == 0
+            torch.cuda.synchronize()
+            intact(y, t, n, gx, gw, gb, s, gz, gv)
+            assert (ws2[size:] == 77).all() and (ws3[size2:] == 77).all()
+    for M, n, k in ((37, 20, 3), (70, 256, 8), (5, 1000, 64), (300, 5, 2)):
+        r, x = layers._Router(k, 1, 1, 1, 2, 0, 1.0), mk(g, M, n).to(dev)
+        w, w_at = marked(M * k)
+        e, e_at = marked(M * k, torch.int64)
+        assert zs._call(dev, lib.zs_route, x.data_ptr(), n, None, r, M, n, 0, w_at, e_at) == 0
+        gx, gx_at = marked(M * n)
+        expert = e[64:-64].clone()
+        r = layers._Router(k, 0, 1, 1, 2, 0, 1.0)
+        assert zs._call(dev, lib.zs_route_backward, torch.ones(M, k, device=dev).data_ptr(), x.data_ptr(), n, expert.data_ptr(), r, M, n, 0, gx_at) == 0
+        torch.cuda.synchronize()
+        assert (w[:64] == 77).all() and (w[-64:] == 77).all() and (e[:64] == 77).all() and (e[-64:] == 77).all()
+        assert not (w[64:-64] == 77).any() and (e[64:-64] < n).all()
+        intact(gx)
 
 
 def test_refusals(dev):
