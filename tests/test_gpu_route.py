@@ -183,6 +183,35 @@ def test_many_rows(dev):
         assert torch.equal(expert[-200:].cpu(), e_ref)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("n,groups,k", [(256, 8, 8), (128, 1, 6), (60, 4, 4), (512, 16, 10), (1024, 1, 12), (16, 1, 2)])
+def test_choice_over_many_rows(dev, score, n, groups, k):
+    """Every choice of 40000 rows, among them rows that fp32 sums cannot tell, against stable sorts in float64."""
+    say("many choices", score, n, groups, k)
+    g = torch.Generator().manual_seed(n + k)
+    M = 40000
+    top = max(1, groups // 2)
+    for dtype, spread in ((F32, 1.5), (BF16, 1.5), (F32, 1e-3), (F32, 1e-6)):
+        x = (spread * torch.randn(M, n, generator=g)).to(dtype).to(dev)
+        bias = (0.3 * spread * torch.randn(n, generator=g)).to(dev)
+        _, expert = zs.zs_route(x, zs.Router(n, k, score=score, groups=groups, top_groups=top), bias)
+        s = torch.sigmoid(x.double()) if score == "sigmoid" else torch.softmax(x.double(), 1)
+        q = s + bias.double()
+        if groups > 1:
+            best = q.view(M, groups, -1).sort(2, descending=True)[0][:, :, :2].sum(2)
+            order = best.sort(dim=1, descending=True, stable=True)[1][:, :top]
+            stay = torch.zeros(M, groups, dtype=torch.bool, device=dev).scatter_(1, order, True)
+            q = q.masked_fill(~stay.repeat_interleave(n // groups, 1), -INF)
+        ref_q, ref_e = q.sort(dim=1, descending=True, stable=True)
+        # rows whose order hangs on the last bits of float64 (a softmax's sum in another order) are left out
+        gap = (ref_q[:, :k] - ref_q[:, 1:k + 1] if n > k else ref_q[:, :k - 1] - ref_q[:, 1:k]).amin(1)
+        sure = gap > 1e-14
+        if groups > 1:
+            sure &= (lambda b: b[:, top - 1] - b[:, top])(best.sort(1, descending=True)[0]) > 1e-14
+        assert sure.float().mean() > 0.9
+        assert torch.equal(expert[sure], ref_e[sure][:, :k]), (dtype, spread)
+
+
 def test_layouts(dev):
     say("layouts")
     g = torch.Generator().manual_seed(8)
