@@ -16,7 +16,7 @@
 //    TB/s of 403 MB.  A wavefront a row, four chunks a lane, no barrier, the next
 //    row's loads in flight; 88 us with a workgroup a row, 120 without the loads ahead,
 //    94 with w read from memory and the deviations formed anew in each pass.
-//  - forward of 8191 x 777 in fp32: 14 us, 3.6 TB/s of 51 MB: no row starts on 16 bytes
+//  - forward of 8191 x 777 in fp32: 12 us, 4.1 TB/s of 51 MB: no row starts on 16 bytes
 //    (23 us with parameters and results channel by channel).
 #include "zs_layers_internal.h"
 #include "zs_row.h"

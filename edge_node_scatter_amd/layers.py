@@ -14,6 +14,7 @@ As in the rest of the package these functions only marshal arguments; there is n
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 import math
 import os
 
@@ -238,6 +239,7 @@ def layer_norm(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = None,
 
 # ---- routing -----------------------------------------------------------------------------------------
 
+@dataclasses.dataclass(frozen=True)
 class Router:
     """How rows choose their experts (include/zs_layers.h has the definition).
 
@@ -246,27 +248,34 @@ class Router:
     whose ``best`` (1 or 2) largest scores have the largest sum.  ``k``
     experts are chosen from those; their scores are the weights, divided by
     their sum if ``renormalise``, times ``scale``."""
+    n_experts: int
+    k: int
+    score: str = "softmax"
+    groups: int = 1
+    top_groups: int = 1
+    best: int = 2
+    renormalise: bool = True
+    scale: float = 1.0
 
-    def __init__(self, n_experts: int, k: int, score: str = "softmax", groups: int = 1,
-                 top_groups: int = 1, best: int = 2, renormalise: bool = True, scale: float = 1.0):
-        if score not in ("softmax", "sigmoid"):
+    def __post_init__(self):
+        if self.score not in ("softmax", "sigmoid"):
             raise ValueError("score must be 'softmax' or 'sigmoid'")
-        if not 1 <= n_experts <= MAX_EXPERTS:
+        if not 1 <= self.n_experts <= MAX_EXPERTS:
             raise ValueError(f"n_experts must be 1 to {MAX_EXPERTS}")
-        if not 1 <= groups <= MAX_EXPERT_GROUPS or n_experts % groups:
+        if not 1 <= self.groups <= MAX_EXPERT_GROUPS or self.n_experts % self.groups:
             raise ValueError(f"groups must be 1 to {MAX_EXPERT_GROUPS} and divide n_experts")
-        if not 1 <= top_groups <= groups:
+        if not 1 <= self.top_groups <= self.groups:
             raise ValueError("top_groups must be 1 to groups")
-        if not 1 <= k <= min(MAX_SLOTS, n_experts // groups * top_groups):
+        if not 1 <= self.k <= min(MAX_SLOTS, self.n_experts // self.groups * self.top_groups):
             raise ValueError(f"k must be 1 to {MAX_SLOTS} and at most the experts that stay")
-        if best not in (1, 2):
+        if self.best not in (1, 2):
             raise ValueError("best must be 1 or 2")
-        if not math.isfinite(scale):
+        if not math.isfinite(self.scale):
             raise ValueError("scale must be finite")
-        self.n_experts, self.k, self.score, self.groups = n_experts, k, score, groups
-        self.top_groups, self.best, self.renormalise, self.scale = (top_groups, best,
-                                                                    bool(renormalise), scale)
-        self._c = _Router(k, score == "sigmoid", groups, top_groups, best, bool(renormalise), scale)
+        # the library's form of it, made once: a router does not change
+        object.__setattr__(self, "_c", _Router(
+            self.k, self.score == "sigmoid", self.groups, self.top_groups, self.best,
+            bool(self.renormalise), self.scale))
 
 
 def _logits(logits: torch.Tensor, router: Router):

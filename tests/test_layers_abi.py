@@ -189,6 +189,9 @@ def test_router_refusals():
         with pytest.raises(ValueError):
             zs.Router(**kw)
     zs.Router(1, 1), zs.Router(1024, 64, groups=64, top_groups=64)
+    r = zs.Router(16, 2)
+    with pytest.raises(AttributeError):   # outputs are sized by what the library was told
+        r.k = 4
 
 
 def test_cpu_tensors_are_refused():
