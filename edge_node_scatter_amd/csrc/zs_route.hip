@@ -526,39 +526,36 @@ __global__ __launch_bounds__(kThreads) void zs_route_kernel(const RouteParams<T>
     // that.
     bool unsettled = false;   // what is no candidate may belong to the slots
     for (int pass = 0;; ++pass) {
-        if (p.bias) {
-            for (int i = l; i < marked; i += L) {
-                const int e = r.candidate[i];
-                const double v = score64(float(logits[e]), p.sigmoid, top, total);
+        for (int i = l; i < marked; i += L) {
+            const int e = r.candidate[i];
+            double v = r.keys[e];
+            if (p.bias) {
+                v = score64(float(logits[e]), p.sigmoid, top, total);
                 r.chance[i] = v;
-                r.key[i] = v + double(p.bias[e]);
+                v += double(p.bias[e]);
             }
-            wave_lds_sync();
+            r.key[i] = v;
         }
+        wave_lds_sync();
         bool close = false;
         unsettled = false;
         for (int i = l; i < marked; i += L) {
-            const int e = r.candidate[i];
-            int rank = 0;
+            const double own = r.key[i];
+            int rank = 0;   // (candidates lie in the order of their index)
+#pragma unroll 4
+            for (int j = 0; j < marked; ++j) {
+                const double o = r.key[j];
+                rank += o > own || (o == own && j < i);
+            }
             if (p.bias) {
-                const double own = r.key[i];
-                for (int j = 0; j < marked; ++j) {
-                    const double o = r.key[j];
-                    rank += o > own || (o == own && r.candidate[j] < e);
-                    close |= j != i && __builtin_fabs(o - own) <= double(tol);
-                }
+                if (pass == 0 && !p.sigmoid)
+                    for (int j = 0; j < marked; ++j)
+                        close |= j != i && __builtin_fabs(r.key[j] - own) <= double(tol);
                 unsettled |= rank == p.k - 1 && marked < have &&
                              !(own >= double(least) + double(tol));
                 if (rank < p.k) r.share[rank] = r.chance[i];
-            } else {
-                const float own = r.keys[e];
-                for (int j = 0; j < marked; ++j) {
-                    const int f = r.candidate[j];
-                    const float o = r.keys[f];
-                    rank += o > own || (o == own && f < e);
-                }
             }
-            if (rank < p.k) r.id[rank] = e;
+            if (rank < p.k) r.id[rank] = r.candidate[i];
         }
         if (pass == 1 || !p.bias || p.sigmoid || __ballot(close) == 0) break;
         total = total64<T, L>(logits, n, top, l);
