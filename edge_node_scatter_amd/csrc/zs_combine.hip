@@ -50,7 +50,7 @@ __global__ __launch_bounds__(kThreads) void zs_combine_kernel(const CombineParam
         u32x4 raw[kLoads];
 #pragma unroll
         for (int q = 0; q < kLoads; ++q)
-            raw[q] = load_chunk(z + (j + q) * p.ldz, chunk, p.c, p.vec);
+            raw[q] = load_any(z + (j + q) * p.ldz, chunk, p.c, p.vec);
 #pragma unroll
         for (int q = 0; q < kLoads; ++q) {
             float f[V];
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kThreads) void zs_combine_kernel(const CombineParam
     }
     for (; j < p.k; ++j) {
         float f[V];
-        Chunk<T>::unpack(load_chunk(z + j * p.ldz, chunk, p.c, p.vec), f);
+        Chunk<T>::unpack(load_any(z + j * p.ldz, chunk, p.c, p.vec), f);
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w[j], f[i], acc[i]);
     }
@@ -95,13 +95,13 @@ __global__ __launch_bounds__(threads_of(L)) void zs_combine_bwd_kernel(const Com
                 next_w[u] = in ? p.weight[row] : 0.0f;
 #pragma unroll
                 for (int n = 0; n < NV; ++n)
-                    next[u][n] = load_chunk<T, true>(p.z + row * p.ldz, l + n * L, in ? c : 0, WHOLE);
+                    next[u][n] = load_any<T, true>(p.z + row * p.ldz, l + n * L, in ? c : 0, WHOLE);
             }
         };
         float g[NV][V];
 #pragma unroll
         for (int n = 0; n < NV; ++n)
-            Chunk<T>::unpack(load_chunk<T, true>(p.gy + t * p.ldg, l + n * L, c, WHOLE), g[n]);
+            Chunk<T>::unpack(load_any<T, true>(p.gy + t * p.ldg, l + n * L, c, WHOLE), g[n]);
         load(0);
         if constexpr (kWaves > 1) __syncthreads();   // the last token's dots are read
         for (int j0 = 0; j0 < p.k; j0 += U) {

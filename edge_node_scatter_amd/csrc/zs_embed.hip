@@ -19,8 +19,10 @@
 //    85 MB: two rounds of dependent reads (positions, rows) in five workgroups a unit.
 //    With the entries read through the index 25 us: its lines come in anew for
 //    every entry.  Parts of runs added one behind the other in LDS: 29 and 8.1 us.
-//  - gradient of 32000 entries over 16384 rows of 2048 in bf16: 32 and 4.9 us, 6.2 TB/s
+//  - gradient of 32000 entries over 16384 rows of 2048 in bf16: 32 and 4.8 us, 6.2 TB/s
 //    of 198 MB, most of it zeros.
+//  - gradient of 21 entries over 42993 rows of 461 in bf16: 21 and 9 us (464: 18 and 9);
+//    29 and 40 with sums of the row's own width, column by column.
 #include "zs_launch.h"
 #include "zs_layers_internal.h"
 #include "zs_row.h"
@@ -62,7 +64,7 @@ __global__ __launch_bounds__(256) void zs_embed_kernel(const EmbedParams<T> p) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 v[u] = from[u] < 0 ? u32x4{0, 0, 0, 0}
-                                   : load_chunk(p.table + from[u] * p.ldt, chunk, p.c, p.vec);
+                                   : load_any(p.table + from[u] * p.ldt, chunk, p.c, p.vec);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t row = base + u * kRows + slot;
@@ -136,7 +138,7 @@ struct GradParams {
     float scale;
     bool vec;
     T* grad;
-    float* sums;      // [pieces][2][c]: of the run that enters a piece, of the one that leaves it
+    float* sums;      // [pieces][2][whole chunks]: of the run that enters a piece, of the one that leaves it
     int32_t* leaves;  // [pieces]: the entry whose run starts in the piece and leaves it, or -1
 };
 
@@ -157,36 +159,23 @@ __device__ inline void store_row(const GradParams<T>& p, int64_t entry, int chun
     for (int i = 0; i < V; ++i) f[i] = v[i] * p.scale;
     store_any(p.grad + entry * p.c, chunk, p.c, p.vec, Chunk<T>::pack(f));
 }
-// fp32 sums of a chunk's columns.
+// fp32 sums of a chunk's columns, in rows of whole chunks.
 template <int V>
-__device__ inline void store_sums(float* row, int chunk, int c, const float (&v)[V]) {
-    if (c % 4 == 0) {
+__device__ inline void store_sums(float* row, int chunk, int chunks, const float (&v)[V]) {
+    if (chunk >= chunks) return;
 #pragma unroll
-        for (int i = 0; i < V; i += 4)
-            if (chunk * V + i < c)
-                *reinterpret_cast<f32x4*>(row + chunk * V + i) =
-                    f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (chunk * V + i < c) row[chunk * V + i] = v[i];
+    for (int i = 0; i < V; i += 4)
+        *reinterpret_cast<f32x4*>(row + chunk * V + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
 }
 template <int V>
-__device__ inline void load_sums(const float* row, int chunk, int c, float (&v)[V]) {
-    if (c % 4 == 0) {
+__device__ inline void load_sums(const float* row, int chunk, int chunks, float (&v)[V]) {
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const f32x4 t = chunk * V + i < c
-                                ? *reinterpret_cast<const f32x4*>(row + chunk * V + i)
-                                : f32x4{0, 0, 0, 0};
+    for (int i = 0; i < V; i += 4) {
+        const f32x4 t = chunk < chunks ? *reinterpret_cast<const f32x4*>(row + chunk * V + i)
+                                       : f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[i + q] = t[q];
-        }
-        return;
+        for (int q = 0; q < 4; ++q) v[i + q] = t[q];
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = chunk * V + i < c ? row[chunk * V + i] : 0.0f;
 }
 
 // The entry whose positions hold q: the last v with offsets[v] <= q (of equal offsets
@@ -204,13 +193,14 @@ __device__ inline int entry_at(const int32_t* offsets, int n_entries, int64_t q)
 template <typename T, int L, bool FEW>
 __global__ __launch_bounds__(kThreads) void zs_embed_grad_kernel(const GradParams<T> p) {
     constexpr int V = Chunk<T>::V, W = kThreads / L;
-    __shared__ int32_t rows[kMaxPositions];
-    __shared__ int32_t entry_of[kMaxPositions + 2];   // one position before and behind
+    constexpr int kPositions = W * kMaxLen < kMaxPositions ? W * kMaxLen : kMaxPositions;
+    __shared__ int32_t rows[kPositions];
+    __shared__ int32_t entry_of[kPositions + 2];   // one position before and behind
     __shared__ int32_t offsets[FEW ? kFewEntries : 1];
     __shared__ __align__(16) float head[W][L * V];
     __shared__ bool through[W];
     const int l = threadIdx.x % L, slot = threadIdx.x / L;
-    const int chunks = (p.c + V - 1) / V;
+    const int chunks = (p.c + V - 1) / V, width = chunks * V;
     const int64_t work = p.pieces * p.blocks, block = p.block0 + blockIdx.x;
     if (block >= work) {   // zeros
         const int64_t v0 = (block - work) * p.zero_rows;
@@ -260,7 +250,8 @@ __global__ __launch_bounds__(kThreads) void zs_embed_grad_kernel(const GradParam
         for (int j = 0; j < kAhead; ++j) {
             at[j] = entry_of[i + j + 1];
             raw[j] = at[j] < 0 ? u32x4{0, 0, 0, 0}
-                               : load_chunk<T, true>(p.gy + int64_t(rows[i + j]) * p.ldg, chunk, p.c, p.vec);
+                               : load_any<T, true>(p.gy + int64_t(rows[i + j]) * p.ldg, chunk, p.c,
+                                                 p.vec);
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
@@ -311,7 +302,7 @@ __global__ __launch_bounds__(kThreads) void zs_embed_grad_kernel(const GradParam
     for (int e = 0; e < V; ++e) head[slot][l * V + e] = entering[e];
     if (l == 0) through[slot] = open;
     __syncthreads();
-    if (slot == 0 && entered) store_sums<V>(p.sums + piece * 2 * p.c, chunk, p.c, entering);
+    if (slot == 0 && entered) store_sums<V>(p.sums + piece * 2 * width, chunk, chunks, entering);
     bool leaves = false;
     if (starts) {
         leaves = true;
@@ -320,7 +311,7 @@ __global__ __launch_bounds__(kThreads) void zs_embed_grad_kernel(const GradParam
             for (int e = 0; e < V; ++e) acc[e] += head[slot + 1][l * V + e];
             leaves = through[slot + 1];
         }
-        if (leaves) store_sums<V>(p.sums + (piece * 2 + 1) * p.c, chunk, p.c, acc);
+        if (leaves) store_sums<V>(p.sums + (piece * 2 + 1) * width, chunk, chunks, acc);
         else store_row(p, cur, chunk, acc);
     }
     // one run at most starts here and leaves
@@ -340,6 +331,7 @@ __global__ __launch_bounds__(kThreads) void zs_embed_join_kernel(const GradParam
     if (entry < 0) return;   // of the whole workgroup
     const int l = threadIdx.x % L, slot = threadIdx.x / L;
     const int chunk = int(block % p.blocks) * L + l;
+    const int chunks = (p.c + V - 1) / V, width = chunks * V;
     int64_t first, last;
     positions(p, first, last);
     int64_t end = p.offsets[int64_t(entry) + 1];
@@ -356,7 +348,8 @@ __global__ __launch_bounds__(kThreads) void zs_embed_join_kernel(const GradParam
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int64_t at = i + j < i1 ? i + j : i;
-            load_sums<V>(p.sums + ((piece + at) * 2 + (at == 0 ? 1 : 0)) * p.c, chunk, p.c, v[j]);
+            load_sums<V>(p.sums + ((piece + at) * 2 + (at == 0 ? 1 : 0)) * width, chunk, chunks,
+                         v[j]);
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
@@ -395,7 +388,7 @@ GradPlan plan_grad(int64_t n_rows, int64_t c, bool bf16) {
     while (g.len > 8 && (n_rows + w * g.len - 1) / (w * g.len) * g.blocks < 1024) g.len /= 2;
     const int64_t count = int64_t(w) * g.len;
     g.pieces = (n_rows + count - 1) / count;
-    g.sums_bytes = g.pieces > 1 ? (size_t(g.pieces) * 2 * size_t(c) * 4 + 255) / 256 * 256 : 0;
+    g.sums_bytes = g.pieces > 1 ? (size_t(g.pieces) * 2 * size_t(chunks * v) * 4 + 255) / 256 * 256 : 0;
     return g;
 }
 

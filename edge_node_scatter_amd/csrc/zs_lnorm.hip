@@ -46,7 +46,7 @@ constexpr int threads_of(int L) { return L > 256 ? L : 256; }
 // channels; the others test each in the row's last chunk.
 template <typename T, bool WHOLE>
 __device__ inline u32x4 load_x(const T* row, int chunk, int c) {
-    return load_chunk<T, true>(row, chunk, c, WHOLE);
+    return load_any<T, true>(row, chunk, c, WHOLE);
 }
 // Calls f(i, whether channel i of the chunk is the row's) for the chunk's channels, if
 // the chunk has any.

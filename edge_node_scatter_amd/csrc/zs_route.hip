@@ -17,8 +17,8 @@
 // fp32 cannot tell, and candidates that may not be all, are settled in fp64 over the whole
 // row, which is slow and rare (with random logits a row in a thousand).
 //
-// Bound by vector instructions, some 550 a row at 256 experts.  Measured on MI355X:
-//  - 16384 rows of 256 experts in 8 groups, 8 slots, bf16: 24 us (8.4 MB are read, 1.6
+// Bound by vector instructions, some 520 a row at 256 experts.  Measured on MI355X:
+//  - 16384 rows of 256 experts in 8 groups, 8 slots, bf16: 22 us (8.4 MB are read, 1.6
 //    written: 2 us at a copy's rate).  All in fp64, a wavefront a row, the largest key
 //    by lane reductions: 48 us; fp32 checked by gaps, whole rows anew in fp64: 35
 //    (rows that went that way ended 15 us after the rest); 16 lanes a row: 30; 64: 33.
