@@ -32,7 +32,8 @@ struct CombineParams {
     float* gw;
 };
 
-template <typename T, int L>
+// WHOLE: rows on 16 bytes of whole chunks.
+template <typename T, int L, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void zs_combine_kernel(const CombineParams<T> p) {
     constexpr int V = Chunk<T>::V, kRows = kThreads / L, kLoads = 4;
     const int64_t block = p.block0 + blockIdx.x;
@@ -45,27 +46,29 @@ __global__ __launch_bounds__(kThreads) void zs_combine_kernel(const CombineParam
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    const auto add = [&](int j, u32x4 raw) {
+        float f[V];
+        Chunk<T>::unpack(settled<T>(raw, chunk, p.c, WHOLE), f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w[j], f[i], acc[i]);
+    };
     int j = 0;
     for (; j + kLoads <= p.k; j += kLoads) {
         u32x4 raw[kLoads];
 #pragma unroll
         for (int q = 0; q < kLoads; ++q)
-            raw[q] = load_any(z + (j + q) * p.ldz, chunk, p.c, p.vec);
+            raw[q] = load_raw(z + (j + q) * p.ldz, chunk, p.c, WHOLE);
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q) {
-            float f[V];
-            Chunk<T>::unpack(raw[q], f);
-#pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w[j + q], f[i], acc[i]);
-        }
+        for (int q = 0; q < kLoads; ++q) add(j + q, raw[q]);
     }
-    for (; j < p.k; ++j) {
-        float f[V];
-        Chunk<T>::unpack(load_any(z + j * p.ldz, chunk, p.c, p.vec), f);
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w[j], f[i], acc[i]);
+    // the rest two at a time (31837 x 2 x 832 in bf16 27 us, 29 one by one)
+    for (; j + 2 <= p.k; j += 2) {
+        const u32x4 raw0 = load_raw(z + j * p.ldz, chunk, p.c, WHOLE);
+        const u32x4 raw1 = load_raw(z + (j + 1) * p.ldz, chunk, p.c, WHOLE);
+        add(j, raw0), add(j + 1, raw1);
     }
-    store_any(p.y + t * p.c, chunk, p.c, p.vec, Chunk<T>::pack(acc));
+    if (j < p.k) add(j, load_raw(z + j * p.ldz, chunk, p.c, WHOLE));
+    store_any(p.y + t * p.c, chunk, p.c, WHOLE, Chunk<T>::pack(acc));
 }
 
 constexpr int threads_of(int L) { return L > kThreads ? L : kThreads; }
@@ -95,14 +98,18 @@ __global__ __launch_bounds__(threads_of(L)) void zs_combine_bwd_kernel(const Com
                 next_w[u] = in ? p.weight[row] : 0.0f;
 #pragma unroll
                 for (int n = 0; n < NV; ++n)
-                    next[u][n] = load_any<T, true>(p.z + row * p.ldz, l + n * L, in ? c : 0, WHOLE);
+                    next[u][n] = load_raw<T, true>(p.z + row * p.ldz, l + n * L, in ? c : 0, WHOLE);
             }
         };
         float g[NV][V];
+        u32x4 raw_g[NV];
 #pragma unroll
         for (int n = 0; n < NV; ++n)
-            Chunk<T>::unpack(load_any<T, true>(p.gy + t * p.ldg, l + n * L, c, WHOLE), g[n]);
+            raw_g[n] = load_raw<T, true>(p.gy + t * p.ldg, l + n * L, c, WHOLE);
         load(0);
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+            Chunk<T>::unpack(settled<T>(raw_g[n], l + n * L, c, WHOLE), g[n]);
         if constexpr (kWaves > 1) __syncthreads();   // the last token's dots are read
         for (int j0 = 0; j0 < p.k; j0 += U) {
             u32x4 raw[U][NV];
@@ -123,7 +130,7 @@ __global__ __launch_bounds__(threads_of(L)) void zs_combine_bwd_kernel(const Com
                 for (int n = 0; n < NV; ++n) {
                     const int at = l + n * L;
                     float z[V];
-                    Chunk<T>::unpack(raw[u][n], z);
+                    Chunk<T>::unpack(settled<T>(raw[u][n], at, c, WHOLE), z);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         dot[u] = __builtin_fmaf(g[n][i], z[i], dot[u]);
@@ -184,7 +191,8 @@ hipError_t run(const CombineArgs& a, hipStream_t stream) {
     const int64_t grid = (a.n_rows + kRows - 1) / kRows * p.blocks;
     return launch_ranges(grid, kThreads, [&](int64_t first, int64_t count) {
         p.block0 = first;
-        zs_combine_kernel<T, L><<<unsigned(count), kThreads, 0, stream>>>(p);
+        if (p.vec) zs_combine_kernel<T, L, true><<<unsigned(count), kThreads, 0, stream>>>(p);
+        else zs_combine_kernel<T, L, false><<<unsigned(count), kThreads, 0, stream>>>(p);
         return hipGetLastError();
     });
 }

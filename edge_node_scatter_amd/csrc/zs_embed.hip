@@ -14,14 +14,15 @@
 // Further workgroups of the same launch write the zeros of entries without a row.
 //
 // Measured on MI355X (a copy reaches 5.15 TB/s):
-//  - lookup of 65536 rows of 1024 in bf16: 37 us, 4.6 TB/s of 168 MB.
+//  - lookup of 65536 rows of 1024 in bf16: 33.6 us, 5.0 TB/s of 168 MB (38 in a kernel that
+//    takes rows of any alignment too).
 //  - gradient of 16 entries over 647170 rows of 32 in fp32: 20.8 and 4.8 us, 4.0 TB/s of
 //    85 MB: two rounds of dependent reads (positions, rows) in five workgroups a unit.
 //    With the entries read through the index 25 us: its lines come in anew for
 //    every entry.  Parts of runs added one behind the other in LDS: 29 and 8.1 us.
 //  - gradient of 32000 entries over 16384 rows of 2048 in bf16: 32 and 4.8 us, 6.2 TB/s
 //    of 198 MB, most of it zeros.
-//  - gradient of 21 entries over 42993 rows of 461 in bf16: 21 and 9 us (464: 18 and 9);
+//  - gradient of 21 entries over 42993 rows of 461 in bf16: 16 and 9 us (464: 15 and 9);
 //    29 and 40 with sums of the row's own width, column by column.
 #include "zs_launch.h"
 #include "zs_layers_internal.h"
@@ -45,7 +46,8 @@ struct EmbedParams {
 };
 
 // L lanes copy a row chunk by chunk, U rows at a time.
-template <typename T, int L, int U>
+// WHOLE: rows on 16 bytes of whole chunks.
+template <typename T, int L, int U, bool WHOLE>
 __global__ __launch_bounds__(256) void zs_embed_kernel(const EmbedParams<T> p) {
     constexpr int V = Chunk<T>::V, kRows = 256 / L;
     const int l = threadIdx.x % L, slot = threadIdx.x / L;
@@ -64,35 +66,41 @@ __global__ __launch_bounds__(256) void zs_embed_kernel(const EmbedParams<T> p) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 v[u] = from[u] < 0 ? u32x4{0, 0, 0, 0}
-                                   : load_any(p.table + from[u] * p.ldt, chunk, p.c, p.vec);
+                                   : load_raw(p.table + from[u] * p.ldt, chunk, p.c, WHOLE);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t row = base + u * kRows + slot;
                 if (row >= p.n_rows) continue;
                 float f[V];
-                Chunk<T>::unpack(v[u], f);
+                Chunk<T>::unpack(settled<T>(v[u], chunk, p.c, WHOLE), f);
 #pragma unroll
                 for (int i = 0; i < V; ++i) f[i] *= p.scale;
                 // a row of no entry is +0 whatever the scale's sign
-                store_any(p.y + row * p.c, chunk, p.c, p.vec,
+                store_any(p.y + row * p.c, chunk, p.c, WHOLE,
                           from[u] < 0 ? v[u] : Chunk<T>::pack(f));
             }
         }
     }
 }
 
-template <typename T, int L>
+template <typename T, int L, bool WHOLE>
 hipError_t run_embed(const EmbedParams<T>& p, hipStream_t stream) {
     constexpr int kRows = 256 / L;
     const int64_t one = (p.n_rows + kRows - 1) / kRows;
     // four rows at a time where that still leaves several workgroups for every unit
     if (one >= 4096) {
         const int64_t want = (one + 3) / 4;
-        zs_embed_kernel<T, L, 4><<<unsigned(want < 1 << 20 ? want : 1 << 20), 256, 0, stream>>>(p);
+        zs_embed_kernel<T, L, 4, WHOLE>
+            <<<unsigned(want < 1 << 20 ? want : 1 << 20), 256, 0, stream>>>(p);
     } else {
-        zs_embed_kernel<T, L, 1><<<unsigned(one), 256, 0, stream>>>(p);
+        zs_embed_kernel<T, L, 1, WHOLE><<<unsigned(one), 256, 0, stream>>>(p);
     }
     return hipGetLastError();
+}
+
+template <typename T, int L>
+hipError_t run_embed(const EmbedParams<T>& p, hipStream_t stream) {
+    return p.vec ? run_embed<T, L, true>(p, stream) : run_embed<T, L, false>(p, stream);
 }
 
 bool on16(const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; }
@@ -246,13 +254,17 @@ __global__ __launch_bounds__(kThreads) void zs_embed_grad_kernel(const GradParam
     for (int i = i0; i < i1; i += kAhead) {
         u32x4 raw[kAhead];
         int32_t at[kAhead];
+        const auto load = [&](bool vec) {
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            at[j] = entry_of[i + j + 1];
-            raw[j] = at[j] < 0 ? u32x4{0, 0, 0, 0}
-                               : load_any<T, true>(p.gy + int64_t(rows[i + j]) * p.ldg, chunk, p.c,
-                                                 p.vec);
-        }
+            for (int j = 0; j < kAhead; ++j) {
+                at[j] = entry_of[i + j + 1];
+                raw[j] = at[j] < 0 ? u32x4{0, 0, 0, 0}
+                                   : load_raw<T, true>(p.gy + int64_t(rows[i + j]) * p.ldg, chunk,
+                                                       p.c, vec);
+            }
+        };
+        if (p.vec) load(true);
+        else load(false);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             if (at[j] != cur) {   // a run ends here
@@ -268,7 +280,7 @@ __global__ __launch_bounds__(kThreads) void zs_embed_grad_kernel(const GradParam
                 inside = false;
             }
             float f[V];
-            Chunk<T>::unpack(raw[j], f);
+            Chunk<T>::unpack(settled<T>(raw[j], chunk, p.c, p.vec), f);
 #pragma unroll
             for (int e = 0; e < V; ++e) acc[e] += f[e];
         }

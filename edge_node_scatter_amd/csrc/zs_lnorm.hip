@@ -46,7 +46,7 @@ constexpr int threads_of(int L) { return L > 256 ? L : 256; }
 // channels; the others test each in the row's last chunk.
 template <typename T, bool WHOLE>
 __device__ inline u32x4 load_x(const T* row, int chunk, int c) {
-    return load_any<T, true>(row, chunk, c, WHOLE);
+    return load_raw<T, true>(row, chunk, c, WHOLE);
 }
 // Calls f(i, whether channel i of the chunk is the row's) for the chunk's channels, if
 // the chunk has any.
@@ -81,7 +81,8 @@ __device__ inline Stats deviations(const u32x4 (&raw)[NV], float (&d)[NV][Chunk<
     float s[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        Chunk<T>::unpack(raw[j], d[j]);   // zeros behind the row's end
+        // zeros behind the row's end
+        Chunk<T>::unpack(settled<T>(raw[j], l + j * L, c, WHOLE), d[j]);
 #pragma unroll
         for (int i = 0; i < V; ++i) s[0] += d[j][i];
     }
@@ -214,7 +215,7 @@ __global__ __launch_bounds__(threads_of(L), (resident<T, L, NV>())) void zs_lnor
             const int at = l + j * L;
             if (at * V >= c) continue;
             float g[V], w[V];
-            Chunk<T>::unpack(in.gy[j], g);
+            Chunk<T>::unpack(settled<T>(in.gy[j], at, c, WHOLE), g);
             weight_of(at, w);
             // behind the row's end g and w are zeros
 #pragma unroll
@@ -234,7 +235,7 @@ __global__ __launch_bounds__(threads_of(L), (resident<T, L, NV>())) void zs_lnor
             const int at = l + j * L;
             if (at * V >= c) continue;
             float g[V], w[V];
-            Chunk<T>::unpack(in.gy[j], g);
+            Chunk<T>::unpack(settled<T>(in.gy[j], at, c, WHOLE), g);
             weight_of(at, w);
 #pragma unroll
             for (int i = 0; i < V; ++i)

@@ -73,9 +73,12 @@ __device__ inline void store_chunk(T* row, int chunk, int c, bool vec, u32x4 v,
         if (i < left) row[chunk * V + i] = u.e[i];
 }
 // The same for rows that may start and end anywhere.  A row's last chunk is loaded as the
-// row's last 16 bytes and moved down in the registers, and stored in up to three
-// pieces: element by element, the lanes that hold a row's end took three times the others'
-// time (layer norm's gradients of 248406 x 95 in bf16 105 us, 44 so).
+// row's last 16 bytes (load_raw) and moved down in the registers where it is used
+// (settled), and stored in up to three pieces: element by element, the lanes that hold a
+// row's end took three times the others' time (layer norm's gradients of 248406 x 95 in
+// bf16 105 us, 44 so).  Moved down where it is loaded, each load would be waited for before
+// the next is asked for, in rows of whole chunks too where one kernel serves both (lookup of
+// 65536 rows of 1024 in bf16 44 us against 33.5, sum of 31837 x 2 x 831 in fp32 77 against 64).
 template <typename T>
 __device__ inline u32x4 move_down(u32x4 v, int elements) {
     constexpr int word = 4 / sizeof(T);   // elements of one
@@ -89,17 +92,22 @@ __device__ inline u32x4 move_down(u32x4 v, int elements) {
     return v;
 }
 template <typename T, bool NT = false>
-__device__ inline u32x4 load_any(const T* row, int chunk, int c, bool vec) {
+__device__ inline u32x4 load_raw(const T* row, int chunk, int c, bool vec) {
     constexpr int V = Chunk<T>::V;
     if (vec) return load_chunk<T, NT>(row, chunk, c, true);
-    const int left = c - chunk * V;
-    if (left <= 0) return u32x4{0, 0, 0, 0};
-    if (c < V) return load_partial(row, left);   // the row is less than a chunk
-    const int back = left < V ? V - left : 0;
+    if (c < V) return load_partial(row, chunk == 0 ? c : 0);   // the row is less than a chunk
+    if (chunk * V >= c) return u32x4{0, 0, 0, 0};
+    const int at = chunk * V < c - V ? chunk * V : c - V;
     u32x4 v;
-    __builtin_memcpy(&v, row + chunk * V - back, 16);
-    if (back) v = move_down<T>(v, back);
+    __builtin_memcpy(&v, row + at, 16);
     return v;
+}
+template <typename T>
+__device__ inline u32x4 settled(u32x4 v, int chunk, int c, bool vec) {
+    constexpr int V = Chunk<T>::V;
+    const int back = (chunk + 1) * V - c;
+    if (vec || c < V || back <= 0) return v;
+    return back < V ? move_down<T>(v, back) : u32x4{0, 0, 0, 0};
 }
 template <typename T>
 __device__ inline void store_any(T* row, int chunk, int c, bool vec, u32x4 v) {
