@@ -564,3 +564,40 @@ def test_offsets_past_32_bits(dev):
     assert torch.equal(y[-30:], (table[:2 * M].view(M, 2, c)[-30:, 0].float() + 2 * table[:2 * M].view(M, 2, c)[-30:, 1].float()).to(BF16))
     gz, gw = zs.zs_combine_backward(y, table[:2 * M], torch.tensor([[1.0, 0.5]], device=dev).expand(M, 2).contiguous())
     assert torch.equal(gz.view(M, 2, c)[-30:, 0], y[-30:]) and torch.equal(gz.view(M, 2, c)[-30:, 1], y[-30:] / 2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("at", [0, 3, 8])
+def test_rows_end_anywhere(dev, dtype, at):
+    """Rows that end at every place of a 16-byte chunk, between elements that are not numbers: none of those counts."""
+    M, k, V = 61, 3, 19
+    for c in (*range(1, 18), *range(260, 269), *range(1017, 1026)):
+        say("rows end anywhere", dtype, at, c)
+        g = gen(c)
+
+        def among(rows, std=1.0):
+            big = torch.full((rows, at + c + 5), float("nan"), dtype=dtype)
+            big[:, at:at + c] = mk(g, rows, c, std=std, dtype=dtype)
+            return big[:, at:at + c], big.to(dev)[:, at:at + c]
+
+        (table, dtable), (gy, dgy), (z, dz), (gt, dgt) = among(V), among(M), among(M * k), among(M)
+        index = tokens(g, M, V)
+        want, bound = ref.embedding(table, index, 1.5)
+        within(zs.zs_embedding(dtable, index.to(dev), 1.5), want, bound(dtype), "lookup")
+        want, bound = ref.embedding_grad(gy, index, V, 1.5)
+        within(zs.zs_embedding_backward(dgy, index.to(dev), V, 1.5), want, bound(dtype), "lookup's gradient")
+        w, b = 1 + 0.2 * mk(g, c), mk(g, c)
+        want, bound = ref.layer_norm(gt, w, b, 1e-5)
+        within(zs.zs_layer_norm(dgt, w.to(dev), b.to(dev)), want, bound(dtype), "layer norm")
+        for got, want, bound, n in zip(zs.zs_layer_norm_backward(dgy, dgt, w.to(dev)), *ref.layer_norm_grads(gy, gt, w, 1e-5), "xwb"):
+            within(got, want, bound(dtype) if n == "x" else bound(), "layer norm's gradient of " + n)
+        for slots in (1, 2, 3):
+            rows, weight = M * k // slots, mk(g, M * k // slots, slots)
+            zz, dzz, t, dt = z[:rows * slots], dz[:rows * slots], *((gy, dgy) if rows <= M else among(rows))
+            t, dt = t[:rows], dt[:rows]
+            want, bound = ref.combine(zz, weight)
+            within(zs.zs_combine(dzz, weight.to(dev)), want, bound(dtype), ("sum", slots))
+            (gz, gw), (bz, bw) = ref.combine_grads(t, zz, weight)
+            got = zs.zs_combine_backward(dt, dzz, weight.to(dev))
+            within(got[0], gz, bz(dtype), ("sum's gradient of rows", slots))
+            within(got[1], gw, bw(), ("sum's gradient of weights", slots))
