@@ -385,8 +385,12 @@ __global__ __launch_bounds__(kThreads) void zs_route_kernel(const RouteParams<T>
     if (p.bias) {
         load_values<float, NV>(p.bias, e0, p.n, 0.0f, b);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
+            // NaN is -inf from here on: a minimum with NaN is the other operand, so that a
+            // group's best would be its second best too
+            b[i] = b[i] > -kInf ? b[i] : -kInf;
             bias_size = b[i] > -kInf ? __builtin_fmaxf(bias_size, __builtin_fabsf(b[i])) : bias_size;
+        }
         bias_size = row_max<L>(bias_size);
     }
     const int64_t row = (p.block0 + blockIdx.x) * (kThreads / L) + slot;
@@ -436,7 +440,7 @@ __global__ __launch_bounds__(kThreads) void zs_route_kernel(const RouteParams<T>
     }
     const float tol = most * 0x1p-19f + (most + bias_size) * 0x1p-22f;
     if (ranked)
-        // -inf or NaN where the bias is
+        // -inf where the bias is
 #pragma unroll
         for (int i = 0; i < NV; ++i) s[i] = x[i] > -kInf ? s[i] + b[i] : -kInf;
     bool here = !bad;   // the lane's group stays, if it holds one
