@@ -189,6 +189,14 @@ __device__ inline Best2 join(Best2 p, float a, float b) {
                  __builtin_fmaxf(__builtin_fminf(p.a, a), __builtin_fmaxf(p.b, b))};
 }
 
+// A group's score from its best two.  One expert that is there makes it a group: the sum
+// of two that leaves fp32 downwards (biases of the type's lowest value as masks) is the
+// lowest value, below every other and beside its like, which fp64 tells apart.
+__device__ inline float score_of(Best2 t, int best) {
+    const float sum = best == 2 && t.b > -kInf ? t.a + t.b : t.a;
+    return t.a > -kInf ? __builtin_fmaxf(sum, -__FLT_MAX__) : -kInf;
+}
+
 // A row's part of LDS: all experts' keys (4 bytes each), the candidates' keys and scores
 // in fp64 (8 each), the slots' scores (8), the groups' scores in fp32, or in fp64 (8), the
 // indices of candidates and slots (4 each) and whether the groups stay (4).
@@ -454,8 +462,7 @@ __global__ __launch_bounds__(kThreads) void zs_route_kernel(const RouteParams<T>
             if (lanes >= 8) t = join(t, dpp<0x141>(t.a), dpp<0x141>(t.b));
             if (lanes >= 16) t = join(t, dpp<0x140>(t.a), dpp<0x140>(t.b));
             if (e0 < p.n)
-                group_score[e0 * p.group_factor >> 20] =
-                    p.best == 2 && t.b > -kInf ? t.a + t.b : t.a;
+                group_score[e0 * p.group_factor >> 20] = score_of(t, p.best);
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i) r.keys[e0 + i] = s[i];
@@ -464,7 +471,7 @@ __global__ __launch_bounds__(kThreads) void zs_route_kernel(const RouteParams<T>
                 Best2 t{-kInf, -kInf};
                 for (int e = g * p.per_group; e < (g + 1) * p.per_group; ++e)
                     t = join(t, r.keys[e], -kInf);
-                group_score[g] = p.best == 2 && t.b > -kInf ? t.a + t.b : t.a;
+                group_score[g] = score_of(t, p.best);
             }
         }
         wave_lds_sync();

@@ -41,3 +41,27 @@ def test_a_bias_that_is_no_number(dev, score):  # noqa: F811
     for dtype in (F32, BF16):
         _, expert, _ = check(torch.zeros(5, 16, dtype=dtype), zs.Router(16, 3, score=score, groups=2), bias, dev)
         assert (expert >= 8).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_whose_sums_leave_fp32(dev, score):  # noqa: F811
+    """The type's lowest value as a mask, and biases whose sum is above its largest: experts that are there all the same."""
+    for n, groups, top in GROUPED:
+        say("large biases", score, n, groups)
+        g = torch.Generator().manual_seed(n + groups)
+        x, k, per = torch.randn(6, n, generator=g), min(4, n // groups), n // groups
+        for best in (1, 2):
+            for keep in (0, 1, top, groups):   # groups with ordinary biases; of the rest all or all but one expert is masked
+                for left in (0, 1):
+                    bias = torch.full((n,), LOW)
+                    for i in torch.randperm(groups, generator=g)[:keep].tolist():
+                        bias[i * per:(i + 1) * per] = 0.1 * torch.randn(per, generator=g)
+                    if left:
+                        bias[per - 1::per] = -0.3
+                    for tops in {top, groups}:
+                        _, expert, _ = check(x, zs.Router(n, k, score=score, groups=groups, top_groups=tops, best=best), bias, dev, what=(n, best, keep, left, tops))
+                        assert (expert < n).all()
+            # sums of two that are both beyond the type, far apart and equal
+            bias = torch.where(torch.rand(n, generator=g) < 0.5, -1.0, 1.0) * (2.0 + 1.4 * torch.rand(n, generator=g)) * 1e38
+            check(x, zs.Router(n, k, score=score, groups=groups, top_groups=top, best=best), bias, dev, what=(n, best, "random"))
+            check(x, zs.Router(n, k, score=score, groups=groups, top_groups=top, best=best), bias.abs().clamp(min=3e38), dev, what=(n, best, "above"))
