@@ -6,9 +6,12 @@
 //   w_j = a s_ij, or a p_j with p_j = s_ij / sum_l s_il
 //
 // backward, the choice held fixed, over the slots that hold an expert:
-//   renormalised: dx_ij = a p_j (gw_j - sum_l gw_l p_l), times 1 - s_ij for sigmoid
+//   renormalised: dx_ij = a p_j (gw_j - m), m = sum_l p_l gw_l, times 1 - s_ij for sigmoid
 //   sigmoid:      dx_ij = a gw_j s_ij (1 - s_ij)
-//   softmax:      dx_e = [e chosen] a gw_j s_e - s_e sum_l a gw_l s_il
+//   softmax:      dx_e = a s_e (G_e - m), m = sum_f s_f G_f, G_e the sum of gw over e's slots
+// Where one expert has nearly all of a row, G_e and m are nearly the same: subtracted in
+// fp32 the rest has no digit left at 18 above the other logits.  Slots' gradients are formed
+// in fp64 as (G_e - h) - sum_f s_f (G_f - h), h the G where most of the sum is.
 //
 // A row lies in the registers of L lanes, NV consecutive experts each.  The choice has to
 // be that of fp64 sums (two experts may differ by less than fp32 holds), at the price of
@@ -603,9 +606,9 @@ __global__ __launch_bounds__(kThreads) void zs_route_kernel(const RouteParams<T>
     }
 }
 
-// Bytes of LDS of a row in the backward: a slot's share and gradient (8 each), its
-// index (4).
-__host__ __device__ inline int back_bytes(int k) { return k * 24; }
+// Bytes of LDS of a row in the backward: a slot's share, its gradient and that of its
+// expert's slots together (8 each), its index (4).
+__host__ __device__ inline int back_bytes(int k) { return k * 32; }
 
 template <typename T, int L, int NV>
 __global__ __launch_bounds__(kThreads) void zs_route_bwd_kernel(const RouteParams<T> p) {
@@ -613,7 +616,8 @@ __global__ __launch_bounds__(kThreads) void zs_route_bwd_kernel(const RouteParam
     const int l = threadIdx.x % L, slot = threadIdx.x / L;
     double* share = reinterpret_cast<double*>(lds + slot * back_bytes(p.k));
     double* grad = share + p.k;
-    int* id = reinterpret_cast<int*>(grad + p.k);
+    double* joint = grad + p.k;
+    int* id = reinterpret_cast<int*>(joint + p.k);
     const bool full = !p.sigmoid && !p.renormalise;   // every logit has a part in the weights
     for (int64_t base = int64_t(blockIdx.x) * (kThreads / L); base < p.n_rows;
          base += int64_t(gridDim.x) * (kThreads / L)) {
@@ -622,68 +626,99 @@ __global__ __launch_bounds__(kThreads) void zs_route_bwd_kernel(const RouteParam
         const T* x = p.x + row * p.ldx;
         float s[NV];
         float top = -kInf;
-        double total = 1.0;
         if (full) {
             load_values<T, NV>(x, l * NV, live ? p.n : 0, -kInf, s);
 #pragma unroll
             for (int i = 0; i < NV; ++i) top = __builtin_fmaxf(top, s[i]);
             top = row_max<L>(top);
-            total = 0.0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                s[i] = s[i] > -kInf ? exp_below(s[i] - top) : 0.0f;
-                total += double(s[i]);
-            }
-            total = row_add<L>(total);
-            const float inv = float(1.0 / total);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) s[i] *= inv;
+            for (int i = 0; i < NV; ++i) s[i] = s[i] > -kInf ? exp_below(s[i] - top) : 0.0f;
         }
-        // the slots' logits, the largest of them, and their shares
+        // the slots' logits, the largest of them with its gradient, and the gradients
         float high = -kInf;
+        double near = 0.0;
+        int live_slots = 0;
         for (int r = l; r < p.k; r += L) {
             const int64_t e = live ? p.chosen[row * p.k + r] : -1;
             const bool in = e >= 0 && e < p.n;
-            id[r] = in ? int(e) : -1;
             const float v = in ? float(x[e]) : -kInf;
-            share[r] = v;
-            high = fmaxf(high, v);
-            grad[r] = in ? double(p.gw[row * p.k + r]) * double(p.scale) : 0.0;
+            const double g = in ? double(p.gw[row * p.k + r]) * double(p.scale) : 0.0;
+            id[r] = in ? int(e) : -1, share[r] = v, grad[r] = g;
+            if (v > high) high = v, near = g;
+            live_slots += in;
         }
-        if (p.renormalise && !p.sigmoid) high = row_max<L>(high);
+        const float own_high = high;
+        high = row_max<L>(high);
+        const bool any = row_ballot<L>(live_slots > 0) != 0;
         wave_lds_sync();
+        if (full) {
+            uint32_t chosen = 0;   // bit i: some slot holds the lane's expert i
+            for (int r = 0; r < p.k; ++r) {
+                const unsigned at = unsigned(id[r] - l * NV);
+                chosen |= (at < NV ? 1u : 0u) << (at & 31);
+            }
+            // theirs are formed in fp64
+#pragma unroll
+            for (int i = 0; i < NV; ++i) s[i] = chosen >> i & 1 ? 0.0f : s[i];
+            // an expert in several slots: the first of them takes all their gradients
+            if (p.k > 1 &&
+                __ballot(row_add<L>(__builtin_popcount(chosen) - live_slots) != 0) != 0) {
+                for (int r = l; r < p.k; r += L) {
+                    double g = 0.0;
+                    bool first = true;
+                    for (int q = 0; q < p.k; ++q)
+                        if (id[q] == id[r]) g += grad[q], first &= q >= r;
+                    joint[r] = first ? g : 0.0;
+                    if (share[r] == double(high)) near = g;
+                    if (!first) share[r] = -double(kInf);
+                }
+                wave_lds_sync();
+                for (int r = l; r < p.k; r += L) grad[r] = joint[r];
+            }
+        }
+        // the gradients' mean is formed as what lies between it and the gradient where most of
+        // the sum is: that of the slot of largest logit, or 0 if that expert is in no slot
+        const uint64_t who = row_ballot<L>(own_high == high);
+        near = __shfl(near, who ? __builtin_ctzll(who) : 0, L);
+        if (full && high < top) near = 0.0;
+        double sum = 0.0, between = 0.0, inv = 1.0;
+        if (full) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) sum += double(s[i]);
+            between = -near * sum;
+        }
         for (int r = l; r < p.k; r += L) {
             const double v = share[r];
             double w = 0.0;
             if (id[r] >= 0) {
                 if (p.sigmoid) w = 1.0 / (1.0 + exp(-v));
-                else if (p.renormalise) w = exp(v - double(high));
-                else w = exp(v - double(top)) / total;
+                else w = exp(v - double(p.renormalise ? high : top));
             }
             share[r] = w;
+            sum += w;
+            between += w * (grad[r] - near);
         }
-        wave_lds_sync();
-        double sum = 1.0;
-        bool any = false;
-        if (p.renormalise) sum = 0.0;
-        for (int r = 0; r < p.k; ++r) {
-            if (p.renormalise) sum += share[r];
-            any |= id[r] >= 0;
+        if (p.renormalise || full) {
+            sum = row_add<L>(sum);
+            if (!(sum > 0.0)) sum = 1.0;   // all shares are 0
+            between = row_add<L>(between);
+            if (p.sigmoid) {   // (the inverse of a sum of tiny scores is above fp64's range)
+                between /= sum;
+            } else {
+                inv = 1.0 / sum;
+                between *= inv;
+            }
         }
-        if (!(sum > 0.0)) sum = 1.0;   // all shares are 0
-        double mean = 0.0;   // of the gradients with the shares
-        if (p.renormalise || full)
-            for (int r = 0; r < p.k; ++r) mean += grad[r] * (share[r] / sum);
-        wave_lds_sync();
         for (int r = l; r < p.k; r += L) {
-            const double w = share[r], g = grad[r];
-            const double d = p.renormalise ? w / sum * (g - mean) : g * w;
-            grad[r] = p.sigmoid ? d * (1.0 - w) : d;
+            const double w = share[r], g = grad[r], rest = (g - near) - between;
+            if (p.sigmoid) grad[r] = (p.renormalise ? w / sum * rest : g * w) * (1.0 - w);
+            else grad[r] = w * inv * rest;
         }
         wave_lds_sync();
         float out[NV];
+        const float each = -float((near + between) * inv);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) out[i] = full && any ? -s[i] * float(mean) : 0.0f;
+        for (int i = 0; i < NV; ++i) out[i] = full && any ? s[i] * each : 0.0f;
         for (int r = 0; r < p.k; ++r) {
             const float d = float(grad[r]);
             const int at = id[r] - l * NV;

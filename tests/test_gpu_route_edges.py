@@ -65,3 +65,77 @@ def test_biases_whose_sums_leave_fp32(dev, score):  # noqa: F811
             bias = torch.where(torch.rand(n, generator=g) < 0.5, -1.0, 1.0) * (2.0 + 1.4 * torch.rand(n, generator=g)) * 1e38
             check(x, zs.Router(n, k, score=score, groups=groups, top_groups=top, best=best), bias, dev, what=(n, best, "random"))
             check(x, zs.Router(n, k, score=score, groups=groups, top_groups=top, best=best), bias.abs().clamp(min=3e38), dev, what=(n, best, "above"))
+
+
+# ---- gradients of confident rows ----------------------------------------------------------------------------------
+
+def scores64(x, sigmoid):
+    return torch.sigmoid(x.double()) if sigmoid else torch.softmax(x.double(), 1)
+
+
+def softmax_grad(gw, x, expert, scale):
+    """Gradient of the logits from that of unnormalised softmax weights, and the size of its terms: with G_e the sum of
+    the gradients of e's slots, dx_e = s_e sum over f of s_f (G_e - G_f), which has no difference of large terms."""
+    s = scores64(x, False)
+    G = torch.zeros_like(s).scatter_add_(1, expert, gw.double() * scale)
+    d = G[:, :, None] - G[:, None, :]
+    return s * (s[:, None, :] * d).sum(2), s * (s[:, None, :] * d.abs()).sum(2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gradient_of_a_confident_softmax(dev, dtype):  # noqa: F811
+    """One expert far ahead: its weight is nearly 1, its gradient the small rest of it."""
+    for n, k in ((8, 1), (20, 1), (64, 1), (64, 3), (160, 6), (300, 2), (1000, 1), (1024, 16)):
+        say("confident softmax", dtype, n, k)
+        g = torch.Generator().manual_seed(n + k)
+        x = torch.randn(48, n, generator=g)
+        margin = torch.tensor([0.0, 4, 8, 10, 12, 14, 16, 18, 20, 25, 30, 36]).repeat(4)
+        x[torch.arange(48), torch.randint(0, n, (48,), generator=g)] += 5 + margin
+        x = x.to(dtype)
+        r = zs.Router(n, k, renormalise=False, scale=1.5)
+        _, expert = zs.zs_route(x.to(dev), r)
+        gw = torch.randn(48, k, generator=g)
+        if k > 2:   # a choice of the caller's own: an expert in two slots
+            expert[::3, 2] = expert[::3, 0]
+        got = zs.zs_route_backward(gw.to(dev), x.to(dev), expert, r).double().cpu()
+        want, size = softmax_grad(gw, x, expert.cpu(), 1.5)
+        # a score that is an fp32 exponential: two ulps (4 half ulps), the rounding of its argument d (|d| half ulps), the
+        # rounding of the factors and the product 4; 88 and more below the largest it is 0
+        d = (x.double() - x.double().amax(1, keepdim=True)).abs().amax(1, keepdim=True)
+        bound = ref.rounded(want, (8 + 2 * d) * ref.HALF * size, dtype)
+        over = ((got - want).abs() - bound).max().item()
+        assert over <= 0, (n, k, over, ((got - want).abs() / bound).max().item())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gradient_of_a_confident_share(dev, dtype, score):  # noqa: F811
+    """Renormalised weights of which one is nearly 1."""
+    for n, k in ((8, 2), (20, 3), (64, 6), (300, 2), (1024, 64)):
+        say("confident share", dtype, score, n, k)
+        g = torch.Generator().manual_seed(n + k)
+        x = torch.randn(36, n, generator=g)
+        margin = torch.tensor([0.0, 8, 12, 16, 20, 25, 30, 36, 40]).repeat(4)
+        if score == "softmax":
+            x[torch.arange(36), torch.randint(0, n, (36,), generator=g)] += margin
+        else:   # (its scores differ by a factor only below 0)
+            x -= margin[:, None]
+            x[torch.arange(36), torch.randint(0, n, (36,), generator=g)] = 0.5
+        x = x.to(dtype)
+        r = zs.Router(n, k, score=score, scale=2.5)
+        _, expert = zs.zs_route(x.to(dev), r)
+        gw = torch.randn(36, k, generator=g)
+        gw[::4] = gw[::4, :1]   # one gradient for all: nothing is left
+        got = zs.zs_route_backward(gw.to(dev), x.to(dev), expert, r).double().cpu()
+        e = expert.cpu()
+        v = x.double().gather(1, e)
+        p = torch.softmax(v if score == "softmax" else torch.nn.functional.logsigmoid(v), 1)
+        rest = 1.0 if score == "softmax" else torch.sigmoid(-v)
+        d = 2.5 * gw.double()
+        d = d[:, :, None] - d[:, None, :]
+        part, size = p * (p[:, None, :] * d).sum(2) * rest, p * (p[:, None, :] * d.abs()).sum(2) * rest
+        want, size = (torch.zeros(36, n, dtype=torch.float64).scatter_(1, e, t) for t in (part, size))
+        # fp64 throughout: 64 additions, some products and exponentials
+        bound = ref.rounded(want, 256 * 2.0 ** -53 * size, dtype) + ref.HALF * want.abs()
+        over = ((got - want).abs() - bound).max().item()
+        assert over <= 0, (n, k, over, ((got - want).abs() / bound).max().item())
