@@ -348,10 +348,10 @@ __device__ inline void groups64(const RouteParams<T>& p, const T* logits, int n,
 
 // The k experts of largest sum in fp64, by rounds over all of them: for rows with more
 // experts too close to call than there are candidates (as with equal logits and no bias
-// yet).
+// yet).  Rows that only share the wavefront with one keep theirs.
 template <typename T, int L>
 __device__ inline void choose64(const RouteParams<T>& p, const T* logits, int n, float top, int l,
-                                const RowLds& r) {
+                                const RowLds& r, bool mine) {
     constexpr double none = -double(kInf);
     const double total = p.sigmoid ? 1.0 : total64<T, L>(logits, n, top, l);
     double last = double(kInf);   // the sum and index of the round before
@@ -370,11 +370,11 @@ __device__ inline void choose64(const RouteParams<T>& p, const T* logits, int n,
         const double m = over_row<L>(best, [](double x, double y) { return x > y ? x : y; });
         last_at = -row_max<L>(best == m && m > none ? -at : -p.n);
         last = m;
-        if (l == 0) r.id[j] = last_at;
+        if (mine && l == 0) r.id[j] = last_at;
         if (last_at == p.n) last = none;
     }
     wave_lds_sync();
-    for (int j = l; j < p.k; j += L)
+    for (int j = l; mine && j < p.k; j += L)
         r.share[j] = r.id[j] < p.n ? score64(float(logits[r.id[j]]), p.sigmoid, top, total) : 0.0;
     wave_lds_sync();
 }
@@ -537,7 +537,7 @@ __global__ __launch_bounds__(kThreads) void zs_route_kernel(const RouteParams<T>
     wave_lds_sync();
     // Their keys in fp64, and their places among each other.  In a softmax with a bias fp64
     // scores need the sum in fp64 as well: where two lie close to each other, once more with
-    // that.
+    // that.  (The row's own decision: its weights have the same bits beside any rows.)
     bool unsettled = false;   // what is no candidate may belong to the slots
     for (int pass = 0;; ++pass) {
         for (int i = l; i < marked; i += L) {
@@ -572,12 +572,14 @@ __global__ __launch_bounds__(kThreads) void zs_route_kernel(const RouteParams<T>
             if (rank < p.k) r.id[rank] = r.candidate[i];
         }
         if (pass == 1 || !p.bias || p.sigmoid || __ballot(close) == 0) break;
-        total = total64<T, L>(logits, n, top, l);
+        const double exact = total64<T, L>(logits, n, top, l);
+        if (row_ballot<L>(close)) total = exact;
         wave_lds_sync();
     }
     for (int j = marked + l; j < p.k; j += L) r.id[j] = p.n;
     wave_lds_sync();
-    if (__ballot(unsettled)) choose64<T, L>(p, logits, n, top, l, r);
+    if (__ballot(unsettled))
+        choose64<T, L>(p, logits, n, top, l, r, row_ballot<L>(unsettled) != 0);
     // the slots' scores or, renormalised in a softmax, exponentials above the largest chosen
     if (!p.bias || (p.renormalise && !p.sigmoid)) {
         float high = top;

@@ -103,9 +103,12 @@ int zs_layer_norm_backward(const void *grad_y, int64_t gy_stride,
  *   weight = scale * s, or scale * s / sum of the chosen s (renormalise)
  *
  * An expert is there if its logit and its bias are above -inf.  Without bias
- * the experts are ranked by their logits, which is the order of s.  s, q, the
- * groups' scores and the weights are formed in fp64 where an fp32 value would
- * decide otherwise; ties go to the lowest index.  A group without an expert
+ * the experts are ranked by their logits, which is the order of s.  The choice
+ * is that of s, q and groups' scores in fp64, ties go to the lowest index.
+ * Weights are formed in fp64 and rounded once, but a softmax's sum over all
+ * experts may be one of fp32 exponentials: without renormalise its weights are
+ * off by up to 10 half ulps.  A row's results do not depend on the other rows
+ * of a call.  A group without an expert
  * does not stay.  A slot that no expert is left for gets the index n_experts
  * and weight 0.  Weights of a row whose chosen scores are all 0 (sigmoid of
  * logits below -709, renormalised) are 0.  A row with a NaN logit, or in a

@@ -139,3 +139,29 @@ def test_gradient_of_a_confident_share(dev, dtype, score):  # noqa: F811
         bound = ref.rounded(want, 256 * 2.0 ** -53 * size, dtype) + ref.HALF * want.abs()
         over = ((got - want).abs() - bound).max().item()
         assert over <= 0, (n, k, over, ((got - want).abs() / bound).max().item())
+
+
+# ---- rows beside others -------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n,k", [(8, 2), (32, 4), (64, 6), (128, 8), (256, 8), (1000, 16)])
+def test_a_row_is_the_same_beside_others(dev, n, k):  # noqa: F811
+    """The bits of a row's weights do not depend on the rows that are computed with it, some of which have experts too
+    close for fp32, and some more of them than there are candidates."""
+    say("rows beside others", n, k)
+    g = torch.Generator().manual_seed(n)
+    M = 96
+    x = 2 * torch.randn(M, n, generator=g)
+    bias = 0.1 * torch.randn(n, generator=g)
+    bias[:2] = 0.9   # among the chosen ones, equal
+    x[::5, 1] = x[::5, 0] + 2.0 ** -22
+    x[3::16] = 0.25 + 2.0 ** -23 * torch.randint(0, 2, (M // 16, n), generator=g)
+    for score in ("softmax", "sigmoid"):
+        for b in (bias, bias.clamp(max=0.9).round(decimals=1)):
+            for renorm in (False, True):
+                r = zs.Router(n, k, score=score, renormalise=renorm)
+                weight, expert = zs.zs_route(x.to(dev), r, b.to(dev))
+                for row in range(M):
+                    w, e = zs.zs_route(x[row:row + 1].to(dev), r, b.to(dev))
+                    assert torch.equal(expert[row:row + 1], e), row
+                    assert torch.equal(weight[row:row + 1].view(torch.int32), w.view(torch.int32)), (score, renorm, row)
+                check(x, r, b, dev, what=(score, renorm))
