@@ -7,8 +7,12 @@
 // 16-byte chunks l, l + L, ...; its sums cross the lanes (and, above a wavefront,
 // LDS).  The mean comes first, then the sums of what is left after it and of its
 // squares; the former corrects the mean, so that a row whose mean is far above its
-// spread keeps its digits.  The backward pass recomputes the statistics from x; the weights' gradients are summed over a
-// workgroup's rows in registers, then over its row slots in LDS, and the
+// spread keeps its digits.  Where the mean's rounding is most of what is left (equal
+// elements far from zero) it is taken off once more: without that step 892 times 7.3e9 gave
+// 0.03 for 0, and gradients whose factor was that of the rounding, not of eps.  The test for
+// it costs 1 to 2 % of the gradients' time (5 at 520 channels in bf16).
+// The backward pass recomputes the statistics from x; the weights' gradients are summed
+// over a workgroup's rows in registers, then over its row slots in LDS, and the
 // workgroups' partial sums are added in order by a second kernel.
 //
 // Bound by memory.  Measured on MI355X (a copy reaches 5.15 TB/s):
@@ -97,10 +101,30 @@ __device__ inline Stats deviations(const u32x4 (&raw)[NV], float (&d)[NV][Chunk<
             q[1] = __builtin_fmaf(d[j][i], d[j][i], q[1]);
         });
     row_sum<L>(q, lds, region);
-    const float rest = q[0] * inv_c;
+    float rest = q[0] * inv_c, square = q[1] * inv_c;
+    // Where the mean's rounding is most of the deviations, the variance below is a difference
+    // without digits: rest is taken off them, as often as it takes.  Once is enough for any
+    // spread; what rounding leaves of equal elements gets 2^-20 or so smaller at a time and
+    // ends when it is nothing against eps.  (Squares of 1e19 are inf, on both sides here.)
+    for (int step = 0; step < 16; ++step) {   // of all the row's lanes alike
+        const bool again = rest * q[0] >= 0.5f * __builtin_fminf(q[1], __FLT_MAX__) &&
+                           square > eps * 0x1p-16f;
+        if (__ballot(again) == 0) break;
+        const float off = again ? rest : 0.0f;
+        q[0] = q[1] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            each<V, WHOLE>(l + j * L, c, [&](int i, bool in) {
+                d[j][i] = in ? d[j][i] - off : 0.0f;
+                q[0] += d[j][i];
+                q[1] = __builtin_fmaf(d[j][i], d[j][i], q[1]);
+            });
+        row_sum<L>(q, lds, region);
+        rest = q[0] * inv_c, square = q[1] * inv_c;
+    }
     Stats t;
     // (the difference of two rounded values can be below 0 where all deviations are the same)
-    const float var = __builtin_fmaf(q[1], inv_c, -rest * rest);
+    const float var = __builtin_fmaf(-rest, rest, square);
     t.r = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps);
     t.shift = -rest * t.r;
     return t;

@@ -75,7 +75,9 @@ int zs_embedding_backward(const void *grad_y, int64_t gy_stride,
  *   x        [n_rows][c], row stride x_stride              (input)
  *   w, b     [c] fp32; b may be NULL (no bias)             (input)
  *   y        [n_rows][c] contiguous                        (output)
- * eps > 0.  zs_layer_norm_backward recomputes the statistics from x; the
+ * eps > 0.  Squares are summed in fp32: a row whose deviations from mu are
+ * above some 1e19 / sqrt(c) has an infinite variance and gives b, and a sum of
+ * x beyond fp32 gives NaN.  zs_layer_norm_backward recomputes the statistics from x; the
  * gradient of b is not written when grad_b is NULL.
  *   grad_y   [n_rows][c], row stride gy_stride             (input)
  *   grad_x   [n_rows][c] contiguous; grad_w, grad_b [c] fp32   (output)
