@@ -115,7 +115,9 @@ def zs_embedding(table: torch.Tensor, index: torch.Tensor, scale: float = 1.0) -
 def zs_embedding_backward(grad_y: torch.Tensor, index: torch.Tensor, n_entries: int,
                           scale: float = 1.0, groups: Csr | None = None) -> torch.Tensor:
     """grad_table (n_entries, c) of zs_embedding, of grad_y's type: the rows of
-    each entry added in fp32 in increasing order, zeros for entries without any.
+    each entry added in fp32, zeros for entries without any.  The order of the
+    additions is fixed by the sizes and groups (the same bits from run to run),
+    but goes by stretches of rows whose sums are joined, not row by row.
 
     The sorted order is ``groups``: the ``Csr`` of ``zs_build_csr(index,
     n_entries)`` or, for rows that already are in the order of their entries,

@@ -42,7 +42,10 @@ int zs_embedding(const void *table, int64_t table_stride, const int64_t *index,
 
 /*
  * zs_embedding_backward -- grad_table[v] = scale * sum of grad_y[i] over the
- * rows i with index[i] == v, in the order of perm.
+ * rows i with index[i] == v.  The sum is taken in fp32 in a fixed order that
+ * depends on the sizes, offsets and perm alone: stretches of an entry's rows one
+ * behind the other as perm has them, then the stretches' sums pairwise.  It is
+ * not the sum of all rows one behind the other.
  *
  *   grad_y   [n_rows][c], row stride gy_stride             (input)
  *   index    [n_rows] int64, as in zs_embedding            (input)
