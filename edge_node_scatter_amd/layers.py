@@ -290,8 +290,9 @@ def _logits(logits: torch.Tensor, router: Router):
 def zs_route(logits: torch.Tensor, router: Router, bias: torch.Tensor | None = None):
     """(weight (M, k) float32, expert (M, k) int64) of logits (M, E), float32 or
     bfloat16, with an optional bias (E,) float32 that has a part in the choice
-    only.  Experts with a logit or bias of -inf are not there; a slot that no
-    expert is left for holds E and weight 0."""
+    only.  Experts with a logit or bias of -inf, or a NaN bias, are not there; a
+    slot that no expert is left for holds E and weight 0.  A row's results do not
+    depend on the other rows of the call."""
     logits, M, E, stride = _logits(logits, router)
     dev = logits.device
     bias = bias if bias is None else _dense(bias, "bias", (E,), torch.float32, dev)

@@ -44,8 +44,8 @@ int zs_embedding(const void *table, int64_t table_stride, const int64_t *index,
  * zs_embedding_backward -- grad_table[v] = scale * sum of grad_y[i] over the
  * rows i with index[i] == v.  The sum is taken in fp32 in a fixed order that
  * depends on the sizes, offsets and perm alone: stretches of an entry's rows one
- * behind the other as perm has them, then the stretches' sums pairwise.  It is
- * not the sum of all rows one behind the other.
+ * behind the other as perm has them, then the stretches' sums with one another.
+ * It is not the sum of all rows one behind the other.
  *
  *   grad_y   [n_rows][c], row stride gy_stride             (input)
  *   index    [n_rows] int64, as in zs_embedding            (input)
@@ -107,17 +107,17 @@ int zs_layer_norm_backward(const void *grad_y, int64_t gy_stride,
  *     of largest q are chosen, in decreasing order
  *   weight = scale * s, or scale * s / sum of the chosen s (renormalise)
  *
- * An expert is there if its logit and its bias are above -inf.  Without bias
- * the experts are ranked by their logits, which is the order of s.  The choice
- * is that of s, q and groups' scores in fp64, ties go to the lowest index.
- * Weights are formed in fp64 and rounded once, but a softmax's sum over all
- * experts may be one of fp32 exponentials: without renormalise its weights are
- * off by up to 10 half ulps.  A row's results do not depend on the other rows
- * of a call.  A group without an expert
- * does not stay.  A slot that no expert is left for gets the index n_experts
- * and weight 0.  Weights of a row whose chosen scores are all 0 (sigmoid of
- * logits below -709, renormalised) are 0.  A row with a NaN logit, or in a
- * softmax a logit of +inf, gets n_experts and NaN in all slots.
+ * An expert is there if its logit and its bias are above -inf (a NaN bias is
+ * not).  Without bias the experts are ranked by their logits, which is the order
+ * of s.  The choice is that of s, q and groups' scores in fp64, ties go to the
+ * lowest index.  Weights are formed in fp64 and rounded once, but a softmax's
+ * sum over all experts may be one of fp32 exponentials: without renormalise its
+ * weights are off by up to 10 half ulps.  A row's results do not depend on the
+ * other rows of a call.  A group without an expert does not stay.  A slot that
+ * no expert is left for gets the index n_experts and weight 0.  Weights of a row
+ * whose chosen scores are all 0 (sigmoid of logits below -709, renormalised) are
+ * 0.  A row with a NaN logit, or in a softmax a logit of +inf, gets n_experts and
+ * NaN in all slots.
  *
  *   logits   [n_rows][n_experts], row stride logits_stride (input)
  *   bias     [n_experts] fp32 or NULL                      (input)
@@ -149,7 +149,10 @@ int zs_route(const void *logits, int64_t logits_stride, const float *bias,
  *   logits   as above; expert [n_rows][k] int64 from zs_route   (input)
  *   grad_logits [n_rows][n_experts] of logits' type, contiguous (output)
  * Slots whose index lies outside [0, n_experts) have no part in it, and a row
- * of such slots only gets zeros.
+ * of such slots only gets zeros.  The chosen experts' gradients are formed in
+ * fp64 and keep their digits where one of them has nearly all of a row; for a
+ * sigmoid 1 - s is a difference of fp64 values, so above a logit of some 20 its
+ * gradient is right to 2^-53 of grad_weight rather than of itself.
  */
 int zs_route_backward(const float *grad_weight, const void *logits,
                       int64_t logits_stride, const int64_t *expert,
