@@ -9,19 +9,22 @@
 // squares; the former corrects the mean, so that a row whose mean is far above its
 // spread keeps its digits.  Where the mean's rounding is most of what is left (equal
 // elements far from zero) it is taken off once more: without that step 892 times 7.3e9 gave
-// 0.03 for 0, and gradients whose factor was that of the rounding, not of eps.  The test for
-// it costs 1 to 2 % of the gradients' time (5 at 520 channels in bf16).
+// 0.03 for 0, and gradients whose factor was that of the rounding, not of eps.
 // The backward pass recomputes the statistics from x; the weights' gradients are summed
 // over a workgroup's rows in registers, then over its row slots in LDS, and the
 // workgroups' partial sums are added in order by a second kernel.
 //
 // Bound by memory.  Measured on MI355X (a copy reaches 5.15 TB/s):
-//  - gradients of 32768 x 2048 in bf16: 70.7 us and 4.8 us for the partial sums, 5.7
+//  - gradients of 32768 x 2048 in bf16: 72 us and 5 us for the partial sums, 5.6
 //    TB/s of 403 MB.  A wavefront a row, four chunks a lane, no barrier, the next
 //    row's loads in flight; 88 us with a workgroup a row, 120 without the loads ahead,
 //    94 with w read from memory and the deviations formed anew in each pass.
+//  - gradients of 4096 x 8192 in fp32: call 79 us, 5.1 TB/s of 403 MB; 97 where lanes behind
+//    the row's end skipped their loads (8192 x 8192 in bf16 92, 95 so).
 //  - forward of 8191 x 777 in fp32: 12 us, 4.1 TB/s of 51 MB: no row starts on 16 bytes
 //    (23 us with parameters and results channel by channel).
+#include <climits>
+
 #include "zs_layers_internal.h"
 #include "zs_row.h"
 
@@ -174,8 +177,22 @@ constexpr int resident() {
     return held <= 56 ? 4 : (held <= 120 ? 3 : 2);
 }
 
+// Chunk `chunk` of a row, which has it.  (A row of less than a chunk is one lane's.)
+template <typename T, int L, bool WHOLE>
+__device__ inline u32x4 load_inside(const T* row, int chunk, int c) {
+    constexpr int V = Chunk<T>::V;
+    if constexpr (WHOLE) return load_chunk<T, true>(row, chunk, INT_MAX, true);
+    if constexpr (L == 1) return load_raw(row, chunk, c, false);
+    const int at = chunk * V < c - V ? chunk * V : c - V;
+    u32x4 v;
+    __builtin_memcpy(&v, row + at, 16);
+    return v;
+}
+
 // A lane's part of a row's inputs as they lie in memory, read once and past the
-// caches.
+// caches.  Lanes behind the row's end load its last chunk and rows behind the last one the
+// last: where loads may be skipped, nobody can count them, and a wait for this row's is one
+// for the next row's too.
 template <int NV>
 struct RowInputs {
     u32x4 x[NV], gy[NV];
@@ -183,11 +200,13 @@ struct RowInputs {
 template <typename T, int L, int NV, bool WHOLE>
 __device__ inline RowInputs<NV> load_row(const NormParams<T>& p, int64_t row, int l) {
     RowInputs<NV> r;
-    const int c = row < p.n_rows ? p.c : 0;
+    const int64_t at = row < p.n_rows ? row : p.n_rows - 1;
+    const int last = (p.c - 1) / Chunk<T>::V;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        r.x[j] = load_x<T, WHOLE>(p.x + row * p.ldx, l + j * L, c);
-        r.gy[j] = load_x<T, WHOLE>(p.gy + row * p.ldg, l + j * L, c);
+        const int chunk = l + j * L < last ? l + j * L : last;
+        r.x[j] = load_inside<T, L, WHOLE>(p.x + at * p.ldx, chunk, p.c);
+        r.gy[j] = load_inside<T, L, WHOLE>(p.gy + at * p.ldg, chunk, p.c);
     }
     return r;
 }
@@ -232,7 +251,11 @@ __global__ __launch_bounds__(threads_of(L), (resident<T, L, NV>())) void zs_lnor
         const RowInputs<NV> in = next;
         next = load_row<T, L, NV, WHOLE>(p, row + step, l);
         float x[NV][V];
-        const Stats t = deviations<T, L, NV, WHOLE>(in.x, x, l, c, p.inv_c, p.eps, lds, region);
+        u32x4 raw[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            raw[j] = !WHOLE || (l + j * L) * V < c ? in.x[j] : u32x4{0, 0, 0, 0};
+        const Stats t = deviations<T, L, NV, WHOLE>(raw, x, l, c, p.inv_c, p.eps, lds, region);
         float s[2] = {0.0f, 0.0f};   // t, t xh
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
