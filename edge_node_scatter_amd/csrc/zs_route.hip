@@ -400,7 +400,7 @@ __global__ __launch_bounds__(kThreads) void zs_route_kernel(const RouteParams<T>
             // NaN is -inf from here on: a minimum with NaN is the other operand, so that a
             // group's best would be its second best too
             b[i] = b[i] > -kInf ? b[i] : -kInf;
-            bias_size = b[i] > -kInf ? __builtin_fmaxf(bias_size, __builtin_fabsf(b[i])) : bias_size;
+            bias_size = __builtin_fmaxf(bias_size, b[i] > -kInf ? __builtin_fabsf(b[i]) : 0.0f);
         }
         bias_size = row_max<L>(bias_size);
     }
@@ -621,124 +621,120 @@ __global__ __launch_bounds__(kThreads) void zs_route_bwd_kernel(const RouteParam
     double* joint = grad + p.k;
     int* id = reinterpret_cast<int*>(joint + p.k);
     const bool full = !p.sigmoid && !p.renormalise;   // every logit has a part in the weights
-    for (int64_t base = int64_t(blockIdx.x) * (kThreads / L); base < p.n_rows;
-         base += int64_t(gridDim.x) * (kThreads / L)) {
-        const int64_t row = base + slot;
-        const bool live = row < p.n_rows;
-        const T* x = p.x + row * p.ldx;
-        float s[NV];
-        float top = -kInf;
-        if (full) {
-            load_values<T, NV>(x, l * NV, live ? p.n : 0, -kInf, s);
+    const int64_t row = (p.block0 + blockIdx.x) * (kThreads / L) + slot;
+    const bool live = row < p.n_rows;
+    const T* x = p.x + row * p.ldx;
+    float s[NV];
+    float top = -kInf;
+    if (full) {
+        load_values<T, NV>(x, l * NV, live ? p.n : 0, -kInf, s);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) top = __builtin_fmaxf(top, s[i]);
-            top = row_max<L>(top);
+        for (int i = 0; i < NV; ++i) top = __builtin_fmaxf(top, s[i]);
+        top = row_max<L>(top);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) s[i] = s[i] > -kInf ? exp_below(s[i] - top) : 0.0f;
-        }
-        // the slots' logits, the largest of them with its gradient, and the gradients
-        float high = -kInf;
-        double near = 0.0;
-        int live_slots = 0;
-        for (int r = l; r < p.k; r += L) {
-            const int64_t e = live ? p.chosen[row * p.k + r] : -1;
-            const bool in = e >= 0 && e < p.n;
-            const float v = in ? float(x[e]) : -kInf;
-            const double g = in ? double(p.gw[row * p.k + r]) * double(p.scale) : 0.0;
-            id[r] = in ? int(e) : -1, share[r] = v, grad[r] = g;
-            if (v > high) high = v, near = g;
-            live_slots += in;
-        }
-        const float own_high = high;
-        high = row_max<L>(high);
-        const bool any = row_ballot<L>(live_slots > 0) != 0;
-        wave_lds_sync();
-        if (full) {
-            uint32_t chosen = 0;   // bit i: some slot holds the lane's expert i
-            for (int r = 0; r < p.k; ++r) {
-                const unsigned at = unsigned(id[r] - l * NV);
-                chosen |= (at < NV ? 1u : 0u) << (at & 31);
-            }
-            // theirs are formed in fp64
-#pragma unroll
-            for (int i = 0; i < NV; ++i) s[i] = chosen >> i & 1 ? 0.0f : s[i];
-            // an expert in several slots: the first of them takes all their gradients
-            if (p.k > 1 &&
-                __ballot(row_add<L>(__builtin_popcount(chosen) - live_slots) != 0) != 0) {
-                for (int r = l; r < p.k; r += L) {
-                    double g = 0.0;
-                    bool first = true;
-                    for (int q = 0; q < p.k; ++q)
-                        if (id[q] == id[r]) g += grad[q], first &= q >= r;
-                    joint[r] = first ? g : 0.0;
-                    if (share[r] == double(high)) near = g;
-                    if (!first) share[r] = -double(kInf);
-                }
-                wave_lds_sync();
-                for (int r = l; r < p.k; r += L) grad[r] = joint[r];
-            }
-        }
-        // the gradients' mean is formed as what lies between it and the gradient where most of
-        // the sum is: that of the slot of largest logit, or 0 if that expert is in no slot
-        const uint64_t who = row_ballot<L>(own_high == high);
-        near = __shfl(near, who ? __builtin_ctzll(who) : 0, L);
-        if (full && high < top) near = 0.0;
-        double sum = 0.0, between = 0.0, inv = 1.0;
-        if (full) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) sum += double(s[i]);
-            between = -near * sum;
-        }
-        for (int r = l; r < p.k; r += L) {
-            const double v = share[r];
-            double w = 0.0;
-            if (id[r] >= 0) {
-                if (p.sigmoid) w = 1.0 / (1.0 + exp(-v));
-                else w = exp(v - double(p.renormalise ? high : top));
-            }
-            share[r] = w;
-            sum += w;
-            between += w * (grad[r] - near);
-        }
-        if (p.renormalise || full) {
-            sum = row_add<L>(sum);
-            if (!(sum > 0.0)) sum = 1.0;   // all shares are 0
-            between = row_add<L>(between);
-            if (p.sigmoid) {   // (the inverse of a sum of tiny scores is above fp64's range)
-                between /= sum;
-            } else {
-                inv = 1.0 / sum;
-                between *= inv;
-            }
-        }
-        for (int r = l; r < p.k; r += L) {
-            const double w = share[r], g = grad[r], rest = (g - near) - between;
-            if (p.sigmoid) grad[r] = (p.renormalise ? w / sum * rest : g * w) * (1.0 - w);
-            else grad[r] = w * inv * rest;
-        }
-        wave_lds_sync();
-        float out[NV];
-        const float each = -float((near + between) * inv);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) out[i] = full && any ? s[i] * each : 0.0f;
+        for (int i = 0; i < NV; ++i) s[i] = s[i] > -kInf ? exp_below(s[i] - top) : 0.0f;
+    }
+    // the slots' logits, the largest of the lane's with its gradient, and the gradients
+    float own = -kInf;
+    double near = 0.0;
+    int live_slots = 0;
+    for (int r = l; r < p.k; r += L) {
+        const int64_t e = live ? p.chosen[row * p.k + r] : -1;
+        const bool in = e >= 0 && e < p.n;
+        const float v = in ? float(x[e]) : -kInf;
+        const double g = in ? double(p.gw[row * p.k + r]) * double(p.scale) : 0.0;
+        id[r] = in ? int(e) : -1, share[r] = v, grad[r] = g;
+        if (v > own) own = v, near = g;
+        live_slots += in;
+    }
+    // of all of the row, or of its slots
+    const float high = full ? top : row_max<L>(own);
+    const bool any = row_ballot<L>(live_slots > 0) != 0;
+    wave_lds_sync();
+    if (full) {
+        uint32_t chosen = 0;   // bit i: some slot holds the lane's expert i
         for (int r = 0; r < p.k; ++r) {
-            const float d = float(grad[r]);
-            const int at = id[r] - l * NV;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (i == at) out[i] += d;
+            const unsigned at = unsigned(id[r] - l * NV);
+            chosen |= (at < NV ? 1u : 0u) << (at & 31);
         }
-        if (live && (l + 1) * NV <= p.n) {
-            T packed[NV];
+        // theirs are formed in fp64
 #pragma unroll
-            for (int i = 0; i < NV; ++i) packed[i] = T(out[i]);
-            __builtin_memcpy(p.gx + row * p.n + l * NV, packed, sizeof packed);
-        } else if (live) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (l * NV + i < p.n) p.gx[row * p.n + l * NV + i] = T(out[i]);
+        for (int i = 0; i < NV; ++i) s[i] = chosen >> i & 1 ? 0.0f : s[i];
+        // an expert in several slots: the first of them takes all their gradients
+        if (p.k > 1 &&
+            __ballot(row_add<L>(__builtin_popcount(chosen) - live_slots) != 0) != 0) {
+            for (int r = l; r < p.k; r += L) {
+                double g = 0.0;
+                bool first = true;
+                for (int q = 0; q < p.k; ++q)
+                    if (id[q] == id[r]) g += grad[q], first &= q >= r;
+                joint[r] = first ? g : 0.0;
+                if (share[r] == double(high)) near = g;
+                if (!first) share[r] = -double(kInf);
+            }
+            wave_lds_sync();
+            for (int r = l; r < p.k; r += L) grad[r] = joint[r];
         }
-        wave_lds_sync();   // before the next row's slots are written
+    }
+    // the gradients' mean is formed as what lies between it and the gradient where most of
+    // the sum is: that of the slot of largest logit, or 0 if that expert is in no slot
+    const uint64_t who = row_ballot<L>(own == high);
+    near = __shfl(near, who ? __builtin_ctzll(who) : 0, L);
+    if (who == 0) near = 0.0;
+    double sum = 0.0, between = 0.0, inv = 1.0;
+    if (full) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) sum += double(s[i]);
+        between = -near * sum;
+    }
+    for (int r = l; r < p.k; r += L) {
+        const double v = share[r];
+        double w = 0.0;
+        if (id[r] >= 0) {
+            if (p.sigmoid) w = 1.0 / (1.0 + exp(-v));
+            else w = exp(v - double(high));
+        }
+        share[r] = w;
+        sum += w;
+        between += w * (grad[r] - near);
+    }
+    if (p.renormalise || full) {
+        sum = row_add<L>(sum);
+        if (!(sum > 0.0)) sum = 1.0;   // all shares are 0
+        between = row_add<L>(between);
+        if (p.sigmoid) {   // (the inverse of a sum of tiny scores is above fp64's range)
+            between /= sum;
+        } else {
+            inv = 1.0 / sum;
+            between *= inv;
+        }
+    }
+    for (int r = l; r < p.k; r += L) {
+        const double w = share[r], g = grad[r], rest = (g - near) - between;
+        if (p.sigmoid) grad[r] = (p.renormalise ? w / sum * rest : g * w) * (1.0 - w);
+        else grad[r] = w * inv * rest;
+    }
+    wave_lds_sync();
+    float out[NV];
+    const float each = -float((near + between) * inv);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) out[i] = full && any ? s[i] * each : 0.0f;
+    for (int r = 0; r < p.k; ++r) {
+        const float d = float(grad[r]);
+        const int at = id[r] - l * NV;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (i == at) out[i] += d;
+    }
+    if (live && (l + 1) * NV <= p.n) {
+        T packed[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) packed[i] = T(out[i]);
+        __builtin_memcpy(p.gx + row * p.n + l * NV, packed, sizeof packed);
+    } else if (live) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (l * NV + i < p.n) p.gx[row * p.n + l * NV + i] = T(out[i]);
     }
 }
 
@@ -755,18 +751,17 @@ hipError_t run(const RouteArgs& a, bool backward, hipStream_t stream) {
     p.gw = a.gw, p.chosen = a.chosen, p.gx = static_cast<T*>(a.gx);
     constexpr int rows = kThreads / L;
     const int64_t want = (a.n_rows + rows - 1) / rows;
-    if (backward) {
-        const unsigned grid = unsigned(want < 1 << 20 ? want : 1 << 20);
-        zs_route_bwd_kernel<T, L, NV>
-            <<<grid, kThreads, size_t(rows) * back_bytes(p.k), stream>>>(p);
-        return hipGetLastError();
-    }
-    // (no loop over rows in the kernel: what the compiler took out of it cost as many registers
+    // (no loop over rows in the kernels: what the compiler took out of it cost as many registers
     // again as the rows' own values)
     return launch_ranges(want, kThreads, [&](int64_t first, int64_t count) {
         p.block0 = first;
-        zs_route_kernel<T, L, NV><<<unsigned(count), kThreads,
-                                    size_t(rows) * row_bytes<L, NV>(p.k, p.groups), stream>>>(p);
+        if (backward)
+            zs_route_bwd_kernel<T, L, NV>
+                <<<unsigned(count), kThreads, size_t(rows) * back_bytes(p.k), stream>>>(p);
+        else
+            zs_route_kernel<T, L, NV>
+                <<<unsigned(count), kThreads, size_t(rows) * row_bytes<L, NV>(p.k, p.groups),
+                   stream>>>(p);
         return hipGetLastError();
     });
 }
