@@ -168,7 +168,7 @@ __global__ __launch_bounds__(threads_of(L)) void zs_lnorm_kernel(const NormParam
 // Wavefronts of the backward on a SIMD: as many as the registers of a lane's part of a
 // row (its values, both sums, and both inputs of this row and the next as they lie in
 // memory) leave room for without spilling.  Rows of 512 lanes take whole workgroups
-// of two wavefronts a SIMD: two of them where they fit (8192 x 8192 in bf16 95 us, 112
+// of two wavefronts a SIMD: two of them where they fit (8192 x 8192 in bf16 95 us then, 112
 // with one; in fp32 two would spill, 104 us against 92).
 template <typename T, int L, int NV>
 constexpr int resident() {

@@ -25,7 +25,9 @@
 //    written: 2 us at a copy's rate).  All in fp64, a wavefront a row, the largest key
 //    by lane reductions: 48 us; fp32 checked by gaps, whole rows anew in fp64: 35
 //    (rows that went that way ended 15 us after the rest); 16 lanes a row: 30; 64: 33.
-//  - gradients of 8191 rows of 160 experts, 6 slots, fp32: 9 us (11 MB).
+//  - gradients of 8191 rows of 160 experts, 6 slots, fp32: 8.5 us (11 MB), 6.8 with
+//    renormalised weights; 65536 rows of 64 experts, one slot: 14 (15 with the same steps in a
+//    loop over rows, whose constants took 28 registers and a wavefront a SIMD).
 #include "zs_launch.h"
 #include "zs_layers_internal.h"
 #include "zs_row.h"
